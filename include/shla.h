@@ -66,6 +66,14 @@ enum {
 #define MLA_ROW 576
 #define MLA_DIM 7168
 
+/* Kinds of cache pages (mla_page_write) and forms of mla_attend_paged. */
+#define MLA_PAGE_BF16 0
+#define MLA_PAGE_E4M3 1
+#define MLA_PAGE_ROW8 656
+#define MLA_FORM_AUTO 0
+#define MLA_FORM_ABSORBED 1
+#define MLA_FORM_EXPANDED 2
+
 /* Human-readable text for a return code.  Static storage; never NULL. */
 const char* mla_status_string(int code);
 
@@ -363,6 +371,109 @@ int mla_query_proj(const mla_bf16_t* x, const mla_bf16_t* wq_a, const mla_bf16_t
                    float eps, const mla_bf16_t* wq_b, const float* rope, int T,
                    const int32_t* pos, int B, mla_bf16_t* q_nope, mla_bf16_t* q_pe, void* ws,
                    size_t ws_bytes, int32_t* status, void* stream);
+
+/*
+ * Paged latent cache.  A pool holds num_pages pages of page_size rows; a row
+ * holds the 576 cached values of one position ("KV compression" page), in
+ * one of two kinds:
+ *   MLA_PAGE_BF16   576 bf16 values (1152 bytes), as in the contiguous cache
+ *   MLA_PAGE_E4M3   656 bytes: 512 latent codes (e4m3: sign, 4 exponent and 3
+ *                   mantissa bits), 4 fp32 scales, 64 bf16 rotary values.  Scale g
+ *                   belongs to latent values 128g .. 128g+127; a value is
+ *                   code * scale.
+ * The pages described on the method's pages are contiguous bf16 only; paging
+ * and the 8-bit kind are this library's own.
+ *   pool         16-byte aligned; page p, row o at pool + p*page_stride + o*row_stride
+ *   page_stride, row_stride   bytes, multiples of 16; row_stride >= 1152 / 656;
+ *                page_stride a multiple of row_stride holding page_size rows;
+ *                fewer than 2^31 - 256 rows in all
+ *   slot         p * page_size + o
+ * No alignment of page_size is required; 16 or more, a multiple of 16, is
+ * fastest for mla_attend_paged on bf16 pages.
+ *
+ * mla_page_write stores rows into slots (MLA_PAGE_E4M3 quantises them as they
+ * are written):
+ *   rows   bf16, row i at rows + i*rstride (rstride in elements, a multiple of 8, >= 576)
+ *   slots  int32 [N]; -1 skips the row, any other slot outside the pool is
+ *          skipped and counted in status[1].  Slots are distinct: of a slot
+ *          listed twice, each 16-byte piece holds one of the two rows'.
+ * The scale of a group is the least power of two 2^n, -117 <= n <= 119, with
+ * max |x| <= 448 * 2^n over the group's finite values; a code is x / scale
+ * (exact) rounded to nearest even, saturated at 448.  An infinity or NaN is
+ * stored as NaN.  A power of two makes code * scale exact in bf16, so the
+ * rounding to a code is the only one.  N >= 0.
+ *
+ * mla_page_read returns the rows of slots as bf16 [N] rows (exactly code *
+ * scale); slot -1, and any other slot outside the pool (counted in
+ * status[1]), gives a row of zeros.
+ *
+ * Both enqueue one kernel and use no workspace.
+ */
+int mla_page_write(const mla_bf16_t* rows, int64_t rstride, const int32_t* slots, int N,
+                   void* pool, int kind, int num_pages, int page_size, int64_t page_stride,
+                   int row_stride, int32_t* status, void* stream);
+int mla_page_read(const void* pool, int kind, int num_pages, int page_size, int64_t page_stride,
+                  int row_stride, const int32_t* slots, int N, mla_bf16_t* rows, int64_t rstride,
+                  int32_t* status, void* stream);
+
+/*
+ * Attention of the new tokens of S sequences over their paged cache, all
+ * cached positions, causal among the new tokens ("Mix and project" page, both
+ * branches of the forward excerpt without the index mask): one token a
+ * sequence (decode), a few (drafted tokens to verify) or a chunk or the whole
+ * of a prompt, mixed freely.  The new tokens' own rows are in the cache
+ * already (mla_page_write).
+ *   Sequence s has the tokens r = cu_q[s] .. cu_q[s+1]-1 and kv_len[s] cached
+ *   positions; position t is row t % page_size of page
+ *   page_table[s, t / page_size].  Its token number i sees the positions
+ *   t < kv_len[s] - (cu_q[s+1] - cu_q[s]) + i + 1:
+ *     s[h,t] = (q_nope[r,h] . W_UK[h] c_t + q_pe[r,h] . kpe_t) * scale
+ *     O[r,h] = sum_t softmax_t(s)[h,t] W_UV[h] c_t
+ *   A token that sees nothing gets O = 0.
+ *   q_nope     bf16 [N, 128, 128], q_pe bf16 [N, 128, 64] (rotated), O bf16 [N, 128, 128]
+ *   wkv_b      bf16 [128, 256, 512], as in mla_decode
+ *   pool, kind, num_pages, page_size, strides: as above (read only)
+ *   page_table int32 [S, max_pages]
+ *   cu_q       int32 [S + 1], cu_q[0] = 0, not decreasing, cu_q[S] <= N: rows of O
+ *              from cu_q[S] on (the padding of a captured call) are left as they are
+ *   kv_len     int32 [S]; a length above max_kv or the table's reach is cut to it
+ *   max_kv     the host's bound on the lengths; sets the workspace's size
+ *   form       MLA_FORM_ABSORBED folds W_UK into the queries and applies W_UV
+ *              after the mix (278,528 flop per token and position).
+ *              MLA_FORM_EXPANDED computes every position's keys and values of
+ *              the 128 heads once (33.6 Mflop a position) and attends to those
+ *              (81,920 flop per token and position).  MLA_FORM_AUTO takes the
+ *              expanded form from an average of 128 new tokens a sequence on.
+ *              The forms agree within rounding.
+ *   ws         at least mla_attend_paged_workspace_bytes(N, S, max_kv, form)
+ *              bytes, 256-byte aligned; contents need not be initialised
+ *   status     optional int32[2].  An entry of page_table outside [0, num_pages)
+ *              for a page below a sequence's length reads as a page of zeros
+ *              and is counted once in status[1].
+ * Cached values at positions below kv_len[s] are taken to be finite: a NaN or
+ * infinity there makes the tokens that see it NaN and may do so to earlier
+ * tokens of the same call.  What the pages hold from kv_len[s] on does not
+ * matter.
+ * 1 <= N <= 65535, 1 <= S <= 65535, 1 <= max_kv <= 2^24,
+ * N * ceil(max_kv / 64) < 2^30 (else MLA_ERR_SHAPE).
+ *
+ * Arithmetic: scores, softmax statistics and outputs accumulate in fp32.
+ * Rounded to bf16, as tensor-core operands: softmax weights; absorbed: q~, the
+ * mixed latent and a split token's partial mixed latents; expanded: keys and
+ * values.  On one device a call gives the same bits every time.
+ *
+ * The kernels of a call are enqueued on `stream`, some under programmatic
+ * dependent launch (as described for mla_decode, with the same stream
+ * semantics for the caller).  The call can be captured into a graph; graphs
+ * that may run at the same time need workspaces of their own.
+ */
+size_t mla_attend_paged_workspace_bytes(int N, int S, int max_kv, int form);
+int mla_attend_paged(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const mla_bf16_t* wkv_b,
+                     const void* pool, int kind, int num_pages, int page_size,
+                     int64_t page_stride, int row_stride, const int32_t* page_table,
+                     int max_pages, const int32_t* cu_q, const int32_t* kv_len, int S, int N,
+                     int max_kv, float scale, int form, mla_bf16_t* O, void* ws, size_t ws_bytes,
+                     int32_t* status, void* stream);
 
 /*
  * Test hook (host only, no device call): the work split of the

@@ -11,6 +11,9 @@ _EXPORTS = (
     "LIB",
     "LIB_PATH",
     "MLAError",
+    "PAGE_ROW8",
+    "mla_attend_paged",
+    "mla_attend_paged_workspace_bytes",
     "mla_cache_write",
     "mla_cache_write_noalloc",
     "mla_cache_write_workspace_bytes",
@@ -24,6 +27,8 @@ _EXPORTS = (
     "mla_index_mask",
     "mla_out_proj",
     "mla_out_proj_workspace_bytes",
+    "mla_page_read",
+    "mla_page_write",
     "mla_query_proj",
     "mla_query_proj_workspace_bytes",
     "mla_rope",

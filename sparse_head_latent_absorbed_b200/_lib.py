@@ -47,6 +47,14 @@ _SIGS = {
                                 _vp, _vp, _c_size, _vp, _vp]),
     "mla_xwt_plan": (_c_int, [_c_int, _c_int, _vp, _vp]),
     "mla_index_mask": (_c_int, [_vp, _c_int, _c_int, _vp, _c_int, _vp, _vp, _vp]),
+    "mla_page_write": (_c_int, [_vp, _c_i64, _vp, _c_int, _vp, _c_int, _c_int, _c_int, _c_i64,
+                                _c_int, _vp, _vp]),
+    "mla_page_read": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_i64, _c_int, _vp, _c_int, _vp,
+                               _c_i64, _vp, _vp]),
+    "mla_attend_paged_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int]),
+    "mla_attend_paged": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_i64, _c_int,
+                                  _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_float,
+                                  _c_int, _vp, _vp, _c_size, _vp, _vp]),
     "mla_gather_rows": (_c_int, [_vp, _c_i64, _c_int, _vp, _c_i64, _c_int, _c_int, _vp,
                                  _c_int, _c_int, _vp, _vp, _vp, _vp]),
 }
@@ -339,3 +347,144 @@ def mla_gather_rows(cache: torch.Tensor, topk: torch.Tensor, end_pos: torch.Tens
                                _p(topk.contiguous()), B, k, _p(end_pos), _p(rows), _p(status),
                                _stream(cache.device)), "mla_gather_rows")
     return rows
+
+
+# ---------------------------------------------------------------------------
+# paged cache
+# ---------------------------------------------------------------------------
+
+PAGE_ROW8 = 656  # bytes of an 8-bit row: 512 codes, 4 fp32 scales, 64 bf16 rotary values
+FORMS = {"auto": 0, "absorbed": 1, "expanded": 2}
+
+
+def _pool(pages: torch.Tensor):
+    """pages -> (pointer, kind, pages, rows per page, page and row strides in bytes)."""
+    if not pages.is_cuda:
+        raise MLAError("pages must be a CUDA tensor")
+    if pages.dtype == torch.bfloat16:
+        kind, width = 0, 576
+    elif pages.dtype == torch.uint8:
+        kind, width = 1, PAGE_ROW8
+    else:
+        raise MLAError("pages must be bfloat16 [P, page_size, 576] or uint8 "
+                       f"[P, page_size, {PAGE_ROW8}], got {pages.dtype}")
+    if pages.dim() != 3 or pages.shape[2] != width or pages.stride(2) != 1:
+        raise MLAError(f"pages must be [P, page_size, {width}] with unit inner stride")
+    P, ps, _ = pages.shape
+    row = pages.stride(1)
+    page = pages.stride(0) if P > 1 else ps * row  # (one page: its stride is never used)
+    if min(row, page) < 0 or max(row, page) > 2 ** 31 - 1:
+        raise MLAError("page strides out of range")
+    size = pages.element_size()
+    return _p(pages), kind, P, ps, page * size, row * size
+
+
+def _int32(t: torch.Tensor, name: str, dim: int, device) -> torch.Tensor:
+    _need(t, torch.int32, name)
+    if t.dim() != dim or not t.is_contiguous():
+        raise MLAError(f"{name} must be contiguous with {dim} dimension(s)")
+    if t.device != device:
+        raise MLAError(f"{name} must be on {device}, got {t.device}")
+    return t
+
+
+def _status(t: Optional[torch.Tensor], device):
+    if t is None:
+        return None
+    if _int32(t, "status", 1, device).numel() < 2:
+        raise MLAError("status must be int32 [2]")
+    return _p(t)
+
+
+def mla_page_write(rows: torch.Tensor, slots: torch.Tensor, pages: torch.Tensor,
+                   status: Optional[torch.Tensor] = None) -> None:
+    """Cache rows bf16 [N, 576] (unit inner stride) into slots int32 [N]
+    (page * page_size + row; -1 skips) of pages: bf16 [P, page_size, 576], or
+    uint8 [P, page_size, 656], which quantises them (see include/shla.h)."""
+    _need(rows, torch.bfloat16, "rows")
+    if rows.dim() != 2 or rows.shape[1] != 576 or rows.stride(1) != 1:
+        raise MLAError("rows must be [N, 576] with unit inner stride")
+    N, dev = rows.shape[0], rows.device
+    if _int32(slots, "slots", 1, dev).shape[0] != N or pages.device != dev:
+        raise MLAError("slots must hold one entry per row, pages be on the rows' device")
+    if N == 0:
+        return
+    pool, kind, P, ps, page, row = _pool(pages)
+    with torch.cuda.device(dev):
+        _check(LIB.mla_page_write(_p(rows), rows.stride(0) if N > 1 else 576, _p(slots), N, pool,
+                                  kind, P, ps, page, row, _status(status, dev), _stream(dev)),
+               "mla_page_write")
+
+
+def mla_page_read(pages: torch.Tensor, slots: torch.Tensor, out: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The rows at slots int32 [N] of pages (either kind) as bf16 [N, 576];
+    slot -1 gives zeros."""
+    dev = pages.device
+    pool, kind, P, ps, page, row = _pool(pages)
+    N = _int32(slots, "slots", 1, dev).shape[0]
+    if out is None:
+        out = torch.empty(N, 576, dtype=torch.bfloat16, device=dev)
+    _need(out, torch.bfloat16, "out")
+    if tuple(out.shape) != (N, 576) or out.stride(1) != 1 or out.device != dev:
+        raise MLAError("out must be [N, 576] with unit inner stride, on the pages' device")
+    if N == 0:
+        return out
+    with torch.cuda.device(dev):
+        _check(LIB.mla_page_read(pool, kind, P, ps, page, row, _p(slots), N, _p(out),
+                                 out.stride(0) if N > 1 else 576, _status(status, dev),
+                                 _stream(dev)), "mla_page_read")
+    return out
+
+
+def mla_attend_paged_workspace_bytes(N: int, S: int, max_kv: int, form: str = "auto") -> int:
+    if form not in FORMS:
+        raise MLAError(f"form must be one of {', '.join(FORMS)}")
+    return int(LIB.mla_attend_paged_workspace_bytes(int(N), int(S), int(max_kv), FORMS[form]))
+
+
+def mla_attend_paged(q_nope: torch.Tensor, q_pe: torch.Tensor, wkv_b: torch.Tensor,
+                     pages: torch.Tensor, page_table: torch.Tensor, cu_q: torch.Tensor,
+                     kv_len: torch.Tensor, scale: float, max_kv: int, form: str = "auto",
+                     out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """New tokens against all cached positions of their sequence, causal among
+    the new ones.  q_nope [N,128,128], q_pe [N,128,64], wkv_b [128,256,512]
+    (bf16); pages as in mla_page_write; page_table int32 [S, max_pages]; cu_q
+    int32 [S + 1] (first token of each sequence); kv_len int32 [S] (cached
+    positions, the new tokens' own among them), none above max_kv; form "auto",
+    "absorbed" or "expanded" -> O bf16 [N,128,128]."""
+    dev = q_nope.device
+    for t, n, shape in ((q_nope, "q_nope", (-1, 128, 128)), (q_pe, "q_pe", (-1, 128, 64)),
+                        (wkv_b, "wkv_b", (128, 256, 512))):
+        _need(t, torch.bfloat16, n)
+        if t.dim() != 3 or t.shape[1:] != shape[1:] or not t.is_contiguous() or t.device != dev:
+            raise MLAError(f"{n} must be contiguous {list(shape)}, on the queries' device")
+    N, S = q_nope.shape[0], kv_len.shape[0] if kv_len.dim() == 1 else -1
+    if q_pe.shape[0] != N or wkv_b.shape[0] != 128:
+        raise MLAError("q_pe must have q_nope's rows, wkv_b 128 heads")
+    _int32(kv_len, "kv_len", 1, dev)
+    if _int32(cu_q, "cu_q", 1, dev).shape[0] != S + 1:
+        raise MLAError("cu_q must have one entry more than kv_len")
+    if _int32(page_table, "page_table", 2, dev).shape[0] != S or pages.device != dev:
+        raise MLAError("page_table must have a row per sequence, pages be on the queries' device")
+    if form not in FORMS:
+        raise MLAError(f"form must be one of {', '.join(FORMS)}")
+    if out is None:
+        out = torch.empty_like(q_nope)
+    _need(out, torch.bfloat16, "out")
+    if out.shape != q_nope.shape or not out.is_contiguous() or out.device != dev:
+        raise MLAError("out must be contiguous [N, 128, 128], on the queries' device")
+    if N == 0 or S == 0:
+        return out
+    pool, kind, P, ps, page, row = _pool(pages)
+    with torch.cuda.device(dev):
+        if ws is None:
+            ws = torch.empty(mla_attend_paged_workspace_bytes(N, S, max_kv, form),
+                             dtype=torch.uint8, device=dev)
+        _check(LIB.mla_attend_paged(_p(q_nope), _p(q_pe), _p(wkv_b), pool, kind, P, ps, page, row,
+                                    _p(page_table), page_table.shape[1], _p(cu_q), _p(kv_len), S,
+                                    N, int(max_kv), float(scale), FORMS[form], _p(out), _p(ws),
+                                    ws.numel(), _status(status, dev), _stream(dev)),
+               "mla_attend_paged")
+    return out

@@ -1,0 +1,55 @@
+// What the two forms of the attention over a paged cache share: the
+// description of the pages and the device-side view of a call's sequences.
+#pragma once
+
+#include "pages.cuh"
+
+namespace shla {
+namespace paged {
+
+constexpr int kH = MLA_HEADS, kC = MLA_LATENT, kR = MLA_ROPE, kD = MLA_NOPE;
+static_assert(MLA_NOPE == 128 && MLA_VDIM == 128, "key and value widths");
+
+template <typename T>
+DEV T* align1024(T* p) {
+  return reinterpret_cast<T*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+
+// A pool of pages and the table of each sequence's pages.
+struct Pool {
+  const uint8_t* base;
+  int kind;               // MLA_PAGE_BF16 or MLA_PAGE_E4M3
+  int num_pages, page_size;
+  int pitch;              // rows from one page to the next
+  int row_stride;         // bytes
+  int rows;               // rows from the first page's first to the last page's last
+  const int32_t* table;   // [S][max_pages]
+  int max_pages;
+};
+
+// The sequences of a call: sequence s has new tokens cu_q[s] .. cu_q[s+1]-1
+// and kv_len[s] cached positions, the new tokens' own among them.
+struct Seqs {
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  int S, N, max_kv;
+
+  // token range of s, whatever cu_q holds, inside [0, N]
+  DEV int q0(int s) const { return min(max(cu_q[s], 0), N); }
+  // positions of s, inside what the bound and the table allow
+  DEV int kv(int s, const Pool& p) const {
+    const long long cap = (long long)p.max_pages * p.page_size;
+    return max(0, min(min(kv_len[s], max_kv), (int)(cap < max_kv ? cap : max_kv)));
+  }
+};
+
+// The row of position `pos` of the sequence whose table row is `t`, or
+// `p.rows` (past the end: reads as zeros) when the table holds no valid page.
+DEV int row_of(const Pool& p, const int32_t* t, int pos) {
+  const int pg = pos / p.page_size;
+  const int page = ld_global_nc_s32_early(t + pg);
+  return page >= 0 && page < p.num_pages ? page * p.pitch + (pos - pg * p.page_size) : p.rows;
+}
+
+}  // namespace paged
+}  // namespace shla

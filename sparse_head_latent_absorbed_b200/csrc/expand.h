@@ -1,0 +1,20 @@
+// The expanded form of the attention over a paged cache (expand.cu).
+#pragma once
+
+#include "attend_paged.cuh"
+
+namespace shla {
+namespace expand {
+
+// Average new tokens per sequence from which MLA_FORM_AUTO expands.  By flops
+// alone the forms meet at 33.6e6 / (278,528 - 81,920) = 171 tokens.
+constexpr int kMinTokens = 1 << 20;
+
+size_t workspace_bytes(int N, int S, int max_kv);
+
+int run(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const mla_bf16_t* wkv_b,
+        const paged::Pool& pool, const paged::Seqs& q, float scale, mla_bf16_t* O, uint8_t* ws,
+        int32_t* status, cudaStream_t st);
+
+}  // namespace expand
+}  // namespace shla

@@ -437,6 +437,7 @@ int mla_page_read(const void* pool, int kind, int num_pages, int page_size, int6
  *   cu_q       int32 [S + 1], cu_q[0] = 0, not decreasing, cu_q[S] <= N: rows of O
  *              from cu_q[S] on (the padding of a captured call) are left as they are
  *   kv_len     int32 [S]; a length above max_kv or the table's reach is cut to it
+ *   scale      softmax scale, > 0 (else MLA_ERR_SHAPE)
  *   max_kv     the host's bound on the lengths; sets the workspace's size
  *   form       MLA_FORM_ABSORBED folds W_UK into the queries and applies W_UV
  *              after the mix (278,528 flop per token and position).
@@ -454,8 +455,11 @@ int mla_page_read(const void* pool, int kind, int num_pages, int page_size, int6
  * infinity there makes the tokens that see it NaN and may do so to earlier
  * tokens of the same call.  What the pages hold from kv_len[s] on does not
  * matter.
- * 1 <= N <= 65535, 1 <= S <= 65535, 1 <= max_kv <= 2^24,
- * N * ceil(max_kv / 64) < 2^30 (else MLA_ERR_SHAPE).
+ * 1 <= N <= 65535, 1 <= S <= 65535, 1 <= max_kv <= 2^24; absorbed: N *
+ * ceil(max_kv / 64) < 2^30; expanded: S * max_kv, each length rounded up to
+ * 128, at most 2^26 (else MLA_ERR_SHAPE).  The expanded form's workspace holds
+ * 1152 bytes for each of those positions and the keys and values of as many
+ * heads as fit 4 GiB, at least 8 (4 KB a position) and at most 128 (64 KB).
  *
  * Arithmetic: scores, softmax statistics and outputs accumulate in fp32.
  * Rounded to bf16, as tensor-core operands: softmax weights; absorbed: q~, the

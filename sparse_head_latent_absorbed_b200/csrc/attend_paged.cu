@@ -1195,8 +1195,10 @@ static int check_sizes(int N, int S, int max_kv, int form) {
   if (N < 1 || N > 65535 || S < 1 || S > 65535 || max_kv < 1 || max_kv > (1 << 24))
     return MLA_ERR_SHAPE;
   if (form < MLA_FORM_AUTO || form > MLA_FORM_EXPANDED) return MLA_ERR_SHAPE;
-  // the flattened list of (token, 64-key tile) is counted in 32 bits
-  if ((int64_t)N * ((max_kv + 63) / 64) > 0x3fffffff) return MLA_ERR_SHAPE;
+  // absorbed: the flattened list of (token, 64-key tile) is counted in 32 bits
+  if (form_of(form, N, S) == MLA_FORM_EXPANDED ? !expand::fits(S, max_kv)
+                                               : (int64_t)N * ((max_kv + 63) / 64) > 0x3fffffff)
+    return MLA_ERR_SHAPE;
   return MLA_OK;
 }
 
@@ -1217,7 +1219,8 @@ extern "C" int mla_attend_paged(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe
   if (int e = pages::check_pool(pool, kind, num_pages, page_size, page_stride, row_stride))
     return e;
   if (int e = check_sizes(N, S, max_kv, form)) return e;
-  if (max_pages < 1) return MLA_ERR_SHAPE;
+  // (written so that a NaN is refused too)
+  if (max_pages < 1 || !(scale > 0.f && scale <= 3.0e38f)) return MLA_ERR_SHAPE;
   if (!aligned16(q_nope) || !aligned16(q_pe) || !aligned16(wkv_b) || !aligned16(O))
     return MLA_ERR_ALIGN;
   if (!ws || !aligned256(ws)) return MLA_ERR_WORKSPACE;

@@ -1,7 +1,917 @@
+// Attention of new tokens over a paged latent cache, expanded form: the keys
+// and values of all 128 heads are computed once for every cached position and
+// the new tokens attend to those,
+//   K[h,t] = [W_UK[h] c_t ; kpe_t],  V[h,t] = W_UV[h] c_t,
+//   O[r,h] = softmax_t((q_nope.K + q_pe.kpe) * scale) V.
+// From about 171 new tokens a sequence on this takes fewer flops than folding
+// W_UK into the queries: 81,920 per token and position and head set against
+// 278,528, for 33.6 Mflop a position.  Four kernels:
+//
+//   layout_kernel   one block: where each sequence's positions go, and the list
+//                   of 256-token query blocks, heaviest first
+//   gather_kernel   the pages' rows, as bf16, one sequence after another
+//   expand_kernel   K and V of a group of heads: a GEMM on CTA pairs
+//   chunk_kernel    the attention of the group's heads
+// The last two run once per group; a group is as many heads as the workspace
+// holds (all 128 up to 65,536 positions).
+#include <math.h>
+
 #include "expand.h"
-namespace shla { namespace expand {
-size_t workspace_bytes(int N, int S, int max_kv) { return 256; }
+#include "tma_map.h"
+
+namespace shla {
+namespace expand {
+
+using paged::kC;
+using paged::kD;
+using paged::kH;
+using paged::kR;
+using paged::Pool;
+using paged::Seqs;
+
+constexpr int kRows = 128;     // positions of a key tile, tokens of a query tile
+constexpr int kBlock = 256;    // tokens of a query block (two tiles)
+constexpr size_t kGroupBytes = size_t(4) << 30;  // keys and values of a group of heads
+
+DEV float u2f(uint32_t x) { return __uint_as_float(x); }
+DEV uint32_t f2u(float x) { return __float_as_uint(x); }
+
+// one lane of a converged warp, the same every time
+DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+
+// ===========================================================================
+// layout
+// ===========================================================================
+
+// A query block: tokens [tok, tok + n) of one sequence; the first sees `lim`
+// positions (possibly none or less), each next one more, none more than kv;
+// position 0 is row `row` of the gathered rows.
+struct Block {
+  int tok, n, lim, kv, row;
+};
+
+struct Layout {
+  int32_t* row;    // [S + 1] first gathered row of each sequence (multiples of 128)
+  int32_t* kv;     // [S]
+  Block* block;    // [N / 256 + S]
+  int32_t* count;  // [1] blocks
+};
+
+DEV int tiles_of(const Block& b, int t) {  // key tiles of query tile t
+  const int n = min(b.n - t * kRows, kRows);
+  if (n <= 0) return 0;
+  const int lim = min(b.kv, b.lim + t * kRows + n - 1);
+  return max(0, (lim + kRows - 1) / kRows);
+}
+
+// exclusive prefix sum over the block's 1024 threads; *total: the sum
+DEV int scan1024(int v, int* part, int* total) {
+  const int tid = threadIdx.x;
+  part[tid] = v;
+  __syncthreads();
+  for (int o = 1; o < 1024; o <<= 1) {
+    const int u = tid >= o ? part[tid - o] : 0;
+    __syncthreads();
+    part[tid] += u;
+    __syncthreads();
+  }
+  const int r = part[tid] - v;
+  *total = part[1023];
+  __syncthreads();
+  return r;
+}
+
+// Blocks are placed by their number of key tiles, most first, in 1024 classes
+// (the order inside a class changes nothing but the order of the work).
+__global__ void __launch_bounds__(1024) layout_kernel(const Seqs q, const Pool pool,
+                                                       const Layout ly, int classes_shift) {
+  __shared__ int part[1024], cls[1024];
+  const int tid = threadIdx.x;
+  const int per = (q.S + 1023) / 1024;
+  const int lo = min(q.S, tid * per), hi = min(q.S, lo + per);
+  int rows = 0;
+  for (int s = lo; s < hi; ++s) {
+    // a sequence without new tokens needs no keys
+    const int kv = q.q0(s + 1) > q.q0(s) ? q.kv(s, pool) : 0;
+    ly.kv[s] = kv;
+    rows += (kv + kRows - 1) / kRows * kRows;
+  }
+  cls[tid] = 0;
+  int total;
+  int at = scan1024(rows, part, &total);
+  for (int s = lo; s < hi; ++s) {
+    ly.row[s] = at;
+    at += (ly.kv[s] + kRows - 1) / kRows * kRows;
+  }
+  if (tid == 0) ly.row[q.S] = total;
+  auto each = [&](auto f) {
+    for (int s = lo; s < hi; ++s) {
+      const int a = q.q0(s), n = q.q0(s + 1) - a;
+      for (int i = 0; i < n; i += kBlock) {
+        Block b;
+        b.tok = a + i;
+        b.n = min(kBlock, n - i);
+        b.kv = ly.kv[s];
+        b.lim = b.kv - n + i + 1;
+        b.row = ly.row[s];
+        const int w = (tiles_of(b, 0) + tiles_of(b, 1)) >> classes_shift;
+        f(b, 1023 - min(1023, w));
+      }
+    }
+  };
+  each([&](const Block&, int c) { atomicAdd(&cls[c], 1); });
+  __syncthreads();
+  const int mine = cls[tid];
+  const int first = scan1024(mine, part, &total);
+  cls[tid] = first;
+  // (ranges of a cu_q that decreases may overlap: no more blocks than there is room for)
+  const int room = q.N / kBlock + q.S;
+  if (tid == 0) *ly.count = min(total, room);
+  __syncthreads();
+  each([&](const Block& b, int c) {
+    const int i = atomicAdd(&cls[c], 1);
+    if (i < room) ly.block[i] = b;
+  });
+}
+
+// ===========================================================================
+// gather: row ly.row[s] + t = position t of sequence s as bf16, zeros from
+// kv[s] to the next multiple of 128 and for entries outside the pool (counted
+// once a page).  One warp per row; bound by memory.
+// ===========================================================================
+template <bool kE4M3>
+__global__ void __launch_bounds__(256) gather_kernel(const Pool pool, const Layout ly, int S,
+                                                      __nv_bfloat16* __restrict__ rows,
+                                                      int32_t* status) {
+  const int lane = threadIdx.x & 31;
+  const int total = ld_global_nc_s32_early(ly.row + S);
+  for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < total; r += gridDim.x * 8) {
+    int a = 0, e = S;  // the last sequence that starts at or before row r
+    while (e - a > 1) {
+      const int m = (a + e) >> 1;
+      if (ly.row[m] <= r) a = m; else e = m;
+    }
+    const int t = r - ly.row[a];
+    uint4 x = make_uint4(0, 0, 0, 0), y = x, pe = x;
+    if (t < ly.kv[a]) {
+      const int row = paged::row_of(pool, pool.table + (long long)a * pool.max_pages, t);
+      if (row == pool.rows) {
+        if (lane == 0 && t % pool.page_size == 0 && status) atomicAdd(status + 1, 1);
+      } else {
+        const uint8_t* src = pool.base + (long long)row * pool.row_stride;
+        if (kE4M3) {
+          const uint4 c = ld_global_nc_v4(src + lane * 16);
+          const float sc = __int_as_float(ld_global_nc_s32_early(
+              reinterpret_cast<const int32_t*>(src + pages::kScaleOff + (lane >> 3) * 4)));
+          if (lane < 8) pe = ld_global_nc_v4(src + pages::kRopeOff + lane * 16);
+          pages::dequant16(c, sc, x, y);
+        } else {
+          x = ld_global_nc_v4(src + lane * 32);
+          y = ld_global_nc_v4(src + lane * 32 + 16);
+          if (lane < 8) pe = ld_global_nc_v4(src + 2 * kC + lane * 16);
+        }
+      }
+    }
+    __nv_bfloat16* dst = rows + (long long)r * MLA_ROW;
+    *reinterpret_cast<uint4*>(dst + lane * 16) = x;
+    *reinterpret_cast<uint4*>(dst + lane * 16 + 8) = y;
+    if (lane < 8) *reinterpret_cast<uint4*>(dst + kC + lane * 8) = pe;
+  }
+}
+
+// ===========================================================================
+// expand_kernel: [K | V][rows, 256] = C [rows, 512] W[h]^T for the group's heads
+//
+// A pair of CTAs multiplies 256 rows with one head's 256 weight rows
+// (tcgen05 cta_group::2, M = 256, N = 256): CTA r holds rows [128r, +128) of C,
+// all 512 columns, for as many heads as its range of the (row block, head)
+// list holds, and streams its half of the weight (r = 0: W_UK, 1: W_UV),
+// 16 KB for every 512 cycles of products.  One CTA alone would have to take in
+// 64 bytes a cycle, which is more than its share of L2.
+// Warps 0-3: epilogue (TMEM -> bf16 -> swizzled shared memory -> TMA store),
+// warp 4: TMA loads, warp 5: MMA (the pair's first CTA issues for both).
+// Two TMEM accumulators, so the epilogue of one tile overlaps the next.
+// ===========================================================================
+namespace gemm {
+constexpr int NB = 4;                       // weight ring depth
+constexpr int CHUNK = kRows * 128;          // 64 columns of 128 rows
+constexpr int OFF_B = 8 * CHUNK;
+constexpr int OFF_OUT = OFF_B + NB * CHUNK; // two output boxes of 64 columns
+constexpr int SMEM = OFF_OUT + 2 * CHUNK + 1024;
+constexpr int THREADS = 192;
+static_assert(SMEM + 512 <= 232448, "shared memory budget");
+
+struct Bars {
+  uint64_t a_full[8], a_empty[8];   // (first CTA) / (both)
+  uint64_t b_full[NB], b_empty[NB];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+}  // namespace gemm
+
+DEV void tmem_alloc2(uint32_t* dst, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(dst)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+DEV void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+DEV void tc_mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// arrive once on the barrier at this offset in both CTAs of the pair when the
+// thread's earlier tcgen05 operations have completed
+DEV void tc_commit2(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// TMA box into this CTA's shared memory, its bytes counted on a barrier of
+// either CTA of the pair
+DEV void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
+      "bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+DEV void tma_store_3d(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::
+                   "l"(reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+DEV void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+// whether `ok` holds in all of warps 0-3 (named barrier 1)
+DEV bool all_of_128(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "bar.red.and.pred p, 1, 128, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+// 32 lanes x 32 bit, 32 consecutive columns
+DEV void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr));
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm::THREADS, 1)
+    expand_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_w,
+                  const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                  const int32_t* __restrict__ total_rows, int head0, int heads, int32_t* status) {
+  using namespace gemm;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = paged::align1024(smem_raw);
+  const uint32_t sbase = smem_u32(smem);
+  __shared__ Bars bars;
+  volatile int* abort = &bars.abort;
+  const uint32_t rank = cluster_ctarank();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // this pair's range of the (256-row block, head) list
+  const long long items =
+      (long long)((ld_global_nc_s32_early(total_rows) + 2 * kRows - 1) / (2 * kRows)) * heads;
+  const int pairs = gridDim.x >> 1, cid = blockIdx.x >> 1;
+  const int lo = (int)(items * cid / pairs), hi = (int)(items * (cid + 1) / pairs);
+
+  if (warp == 5) tmem_alloc2(&bars.tmem_base, 512);
+  if (tid == 0) {
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&bars.a_full[i], 1);
+      mbar_init(&bars.a_empty[i], 1);
+    }
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(&bars.b_full[i], 1);
+      mbar_init(&bars.b_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.acc_full[i], 1);
+      mbar_init(&bars.acc_empty[i], 8);  // four epilogue warps of each CTA
+    }
+    mbar_init(&bars.drain, 1);
+    bars.abort = 0;
+    fence_mbarrier_init_cluster();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_base;
+
+  if (warp == 4) {
+    // ---------------- loads: each CTA its own operands ----------------
+    // The first CTA's barriers count the bytes of both; it alone arrives.
+    const uint32_t a_full0 = mapa_shared(smem_u32(&bars.a_full[0]), 0);
+    const uint32_t b_full0 = mapa_shared(smem_u32(&bars.b_full[0]), 0);
+    int ring = 0, nblk = 0, prev = -1;
+    bool ok = true;
+    for (int it = lo; it < hi && ok; ++it) {
+      const int rb = it / heads, h = it - rb * heads;
+      const bool fresh = rb != prev;
+      for (int kc = 0; kc < 8 && ok; ++kc) {
+        if (fresh) {
+          // the previous block's products with this chunk are done
+          ok = warp_wait(&bars.a_empty[kc], (nblk & 1) ^ 1, abort, status);
+          if (!ok) break;
+          if (lane == 0) {
+            if (rank == 0) mbar_arrive_expect_tx(&bars.a_full[kc], 2 * CHUNK);
+            tma_load_2d_pair(sbase + kc * CHUNK, &map_c, kc * 64, rb * 2 * kRows + rank * kRows,
+                             a_full0 + kc * 8);
+          }
+        }
+        const int s = ring % NB;
+        ok = warp_wait(&bars.b_empty[s], ((ring / NB) & 1) ^ 1, abort, status);
+        if (!ok) break;
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive_expect_tx(&bars.b_full[s], 2 * CHUNK);
+          tma_load_2d_pair(sbase + OFF_B + s * CHUNK, &map_w, kc * 64,
+                           (head0 + h) * 256 + rank * 128, b_full0 + s * 8);
+        }
+        ++ring;
+      }
+      if (fresh) ++nblk;
+      prev = rb;
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    // ---------------- MMA ----------------
+    if (rank == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(256, 256, 0, 0);
+      int ring = 0, nblk = 0, prev = -1;
+      bool ok = true;
+      for (int it = lo; it < hi && ok; ++it) {
+        const int i = it - lo, buf = i & 1, rb = it / heads;
+        const bool fresh = rb != prev;
+        const bool last = it + 1 == hi || (it + 1) / heads != rb;
+        ok = warp_wait<true>(&bars.acc_empty[buf], ((i >> 1) & 1) ^ 1, abort, status);
+        for (int kc = 0; kc < 8 && ok; ++kc) {
+          if (fresh) ok = warp_wait<true>(&bars.a_full[kc], nblk & 1, abort, status);
+          const int s = ring % NB;
+          ok = ok && warp_wait<true>(&bars.b_full[s], (ring / NB) & 1, abort, status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t al = desc_lo(sbase + kc * CHUNK, 16);
+          const uint32_t bl = desc_lo(sbase + OFF_B + s * CHUNK, 16);
+          if (elect_one()) {
+            constexpr uint32_t hi128 = desc_hi(1024, kSwizzle128B);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              tc_mma2(tmem + buf * 256, desc_join(al + ks * 2, hi128),
+                      desc_join(bl + ks * 2, hi128), idesc, (kc > 0 || ks > 0) ? 1u : 0u);
+            tc_commit2(&bars.b_empty[s]);
+            if (last) tc_commit2(&bars.a_empty[kc]);
+            if (kc == 7) tc_commit2(&bars.acc_full[buf]);
+          }
+          __syncwarp();
+          ++ring;
+        }
+        if (fresh) ++nblk;
+        prev = rb;
+      }
+      // everything issued so far has finished before TMEM is released
+      if (elect_one()) tc_commit2(&bars.drain);
+      __syncwarp();
+      warp_wait<true>(&bars.drain, 0, nullptr, status);
+    }
+  } else {
+    // ---------------- epilogue: this CTA's 128 rows ----------------
+    const uint32_t acc_empty0 = mapa_shared(smem_u32(&bars.acc_empty[0]), 0);
+    const int row = warp * 32 + lane;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    for (int it = lo; it < hi; ++it) {
+      const int i = it - lo, buf = i & 1, rb = it / heads, h = it - rb * heads;
+      // (the four warps leave together, so that none waits for another below)
+      if (!all_of_128(warp_wait<true>(&bars.acc_full[buf], (i >> 1) & 1, abort, status))) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int b = 0; b < 4; ++b) {  // keys 0-63, 64-127, values 0-63, 64-127
+        uint32_t r[64];
+        tmem_ld32(tmem + lanes + buf * 256 + b * 64, r);
+        tmem_ld32(tmem + lanes + buf * 256 + b * 64 + 32, r + 32);
+        tc_wait_ld();
+        if (b == 3) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(acc_empty0 + buf * 8);
+        }
+        // the store before last has read its box
+        if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const uint32_t box = sbase + OFF_OUT + (b & 1) * CHUNK;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          st_shared_v4(box + sw128_off(row, c), pack_bf16x2(u2f(r[8 * c]), u2f(r[8 * c + 1])),
+                       pack_bf16x2(u2f(r[8 * c + 2]), u2f(r[8 * c + 3])),
+                       pack_bf16x2(u2f(r[8 * c + 4]), u2f(r[8 * c + 5])),
+                       pack_bf16x2(u2f(r[8 * c + 6]), u2f(r[8 * c + 7])));
+        fence_proxy_async_smem();
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (tid == 0) {
+          tma_store_3d(b < 2 ? &map_k : &map_v, (b & 1) * 64, rb * 2 * kRows + rank * kRows, h, box);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+      }
+    }
+    if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (*abort) {
+    // a warp that gave up may leave loads in flight, which land within
+    // microseconds: a millisecond before the pair leaves
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000) {
+    }
+  }
+  cluster_sync_all();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc2(tmem, 512);
+  }
+  cluster_sync_all();  // neither CTA leaves before both have released
+}
+
+// ===========================================================================
+// chunk_kernel: attention of a query block (two tiles of 128 tokens) of one
+// head over its sequence's key tiles of 128 positions
+//   S_t = Q_t K^T   M = 128 tokens, N = 128, K = 192, both from shared memory
+//   O_t += P_t V    M = 128, N = 2 x 64, K = 128, P from TMEM
+// with one fp32 online softmax per token (a thread per token: no shuffles).
+// Two query tiles share every key tile: while one's scores are in the softmax
+// the tensor cores work for the other.  P overlays its scores, rounded to bf16
+// as a tensor-core operand (the row sum is of the fp32 weights).
+// Warps 0-3 and 4-7: softmax and output of tile 0 and 1; warp 8: TMA; warp 9:
+// MMA.  Keys and values arrive in 16 KB units (64 columns of 128 positions;
+// key: two of the non-rotary part and one rotary, value: two) through a ring
+// of eight.
+// TMEM: scores [0,128) [128,256), outputs [256,384) [384,512).
+// ===========================================================================
+namespace attn {
+constexpr int UNIT = kRows * 128;
+constexpr int NU = 8;
+constexpr int OFF_U = 6 * UNIT;  // after two query tiles of three units
+constexpr int SMEM = OFF_U + NU * UNIT + 1024;
+constexpr int THREADS = 384;  // (two idle warps complete the third register group)
+// register split (168 per thread at launch): 2 x 208 + 88 = 3 x 168
+constexpr int REGS_SOFT = 208, REGS_REST = 88;
+static_assert(2 * REGS_SOFT + REGS_REST <= 3 * 168, "register split");
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+static_assert(SMEM + 512 <= 232448, "shared memory budget");
+
+struct Bars {
+  uint64_t q_full[2], q_free[2];
+  uint64_t full[NU], empty[NU];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+}  // namespace attn
+
+// pairs of fp32 values in one 64-bit register: one instruction for two
+DEV uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+DEV void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+DEV uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__global__ void __launch_bounds__(attn::THREADS, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_constant__ CUtensorMap map_qr,
+                 const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_r,
+                 const __grid_constant__ CUtensorMap map_v, const Layout ly, int head0, int heads,
+                 float scale_log2, __nv_bfloat16* __restrict__ O, int32_t* status) {
+  using namespace attn;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = paged::align1024(smem_raw);
+  const uint32_t sbase = smem_u32(smem);
+  __shared__ Bars bars;
+  volatile int* abort = &bars.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int items = ld_global_nc_s32_early(ly.count) * heads;
+
+  if (warp == 9) {
+    tmem_alloc(&bars.tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars.q_full[t], 1);
+      mbar_init(&bars.q_free[t], 1);
+      mbar_init(&bars.s_full[t], 1);
+      mbar_init(&bars.p_full[t], 4);
+      mbar_init(&bars.o_full[t], 1);
+    }
+    for (int i = 0; i < NU; ++i) {
+      mbar_init(&bars.full[i], 1);
+      mbar_init(&bars.empty[i], 1);
+    }
+    mbar_init(&bars.drain, 1);
+    bars.abort = 0;
+    fence_mbarrier_init_cluster();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_base;
+
+  if (warp >= 10) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));  // (idle)
+  } else if (warp == 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
+    // ---------------- TMA ----------------
+    int u = 0, qn[2] = {0, 0};
+    bool ok = true;
+    auto unit = [&](const CUtensorMap* map, int x, int y, int z, bool three) {
+      ok = ok && warp_wait(&bars.empty[u % NU], ((u / NU) & 1) ^ 1, abort, status);
+      if (!ok) return;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars.full[u % NU], UNIT);
+        const uint32_t dst = sbase + OFF_U + (u % NU) * UNIT;
+        if (three) tma_load_3d(dst, map, x, y, z, &bars.full[u % NU]);
+        else tma_load_2d(dst, map, x, y, &bars.full[u % NU]);
+      }
+      ++u;
+    };
+    for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+      const int h = it % heads;
+      const Block b = ly.block[it / heads];
+      const int nt[2] = {tiles_of(b, 0), tiles_of(b, 1)};
+      const int n = max(nt[0], nt[1]);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (nt[t] == 0) continue;
+        ok = ok && warp_wait(&bars.q_free[t], (qn[t] & 1) ^ 1, abort, status);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars.q_full[t], 3 * UNIT);
+          const uint32_t dst = sbase + t * 3 * UNIT;
+          tma_load_3d(dst, &map_qn, 0, head0 + h, b.tok + t * kRows, &bars.q_full[t]);
+          tma_load_3d(dst + UNIT, &map_qn, 64, head0 + h, b.tok + t * kRows, &bars.q_full[t]);
+          tma_load_3d(dst + 2 * UNIT, &map_qr, 0, head0 + h, b.tok + t * kRows, &bars.q_full[t]);
+        }
+        ++qn[t];
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        const int r = b.row + j * kRows;
+        unit(&map_k, 0, r, h, true);
+        unit(&map_k, 64, r, h, true);
+        unit(&map_r, 0, r, 0, false);
+        unit(&map_v, 0, r, h, true);
+        unit(&map_v, 64, r, h, true);
+      }
+    }
+    // on an abort, the loads still in flight land before the CTA can leave
+    for (int i = max(0, u - NU); i < u; ++i)
+      warp_wait(&bars.full[i % NU], (i / NU) & 1, nullptr, nullptr);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      if (qn[t]) warp_wait(&bars.q_full[t], (qn[t] - 1) & 1, nullptr, nullptr);
+  } else if (warp == 9) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
+    // ---------------- MMA ----------------
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
+    constexpr uint32_t idesc_o = idesc_bf16_f32(128, 64, 0, 1);
+    constexpr uint32_t hi128 = desc_hi(1024, kSwizzle128B);
+    int u0 = 0;                     // ring position of the item's first unit
+    int qn[2] = {0, 0}, pn[2] = {0, 0};
+    bool ok = true;
+    auto have = [&](int u) {
+      return warp_wait(&bars.full[u % NU], (u / NU) & 1, abort, status);
+    };
+    // scores of query tile t and key tile at units u .. u+2; `done`: the
+    // key tile's last use; `lastq`: the query tile's last use
+    auto score = [&](int t, int u, bool done, bool lastq) {
+#pragma unroll
+      for (int c = 0; c < 3; ++c) {
+        ok = ok && have(u + c);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t al = desc_lo(sbase + (t * 3 + c) * UNIT, 16);
+        const uint32_t bl = desc_lo(sbase + OFF_U + ((u + c) % NU) * UNIT, 16);
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            tc_mma(tmem + t * 128, desc_join(al + ks * 2, hi128), desc_join(bl + ks * 2, hi128),
+                   idesc_s, (c > 0 || ks > 0) ? 1u : 0u);
+          if (done) tc_commit(&bars.empty[(u + c) % NU]);
+        }
+        __syncwarp();
+      }
+      if (elect_one()) {
+        tc_commit(&bars.s_full[t]);
+        if (lastq) tc_commit(&bars.q_free[t]);
+      }
+      __syncwarp();
+    };
+    auto value = [&](int t, int u, bool first, bool done, bool last) {
+      ok = ok && warp_wait(&bars.p_full[t], pn[t] & 1, abort, status);
+      ++pn[t];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        ok = ok && have(u + c);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t bl = desc_lo(sbase + OFF_U + ((u + c) % NU) * UNIT, UNIT);
+        const uint32_t d = tmem + 256 + t * 128 + c * 64, a = tmem + t * 128;
+        if (elect_one()) {
+          if (first) tc_mma_tmem_a_c<false>(d, a, desc_join(bl, hi128), idesc_o);
+          else tc_mma_tmem_a_c<true>(d, a, desc_join(bl, hi128), idesc_o);
+#pragma unroll
+          for (int ks = 1; ks < 8; ++ks)
+            tc_mma_tmem_a_c<true>(d, a + ks * 8, desc_join(bl + ks * (2048 >> 4), hi128), idesc_o);
+          if (done) tc_commit(&bars.empty[(u + c) % NU]);
+        }
+        __syncwarp();
+      }
+      if (last && elect_one()) tc_commit(&bars.o_full[t]);
+      __syncwarp();
+    };
+    for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+      const Block b = ly.block[it / heads];
+      const int nt[2] = {tiles_of(b, 0), tiles_of(b, 1)};
+      const int n = max(nt[0], nt[1]);
+      // tile t is the last to use key tile j when the other is not active there
+      auto lastuse = [&](int t, int j) { return t == 1 || j >= nt[1]; };
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (nt[t] > 0 && ok) {
+          ok = warp_wait(&bars.q_full[t], qn[t] & 1, abort, status);
+          ++qn[t];
+          if (ok) score(t, u0, lastuse(t, 0), nt[t] == 1);
+        }
+      for (int j = 0; j < n && ok; ++j)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (j < nt[t] && ok)
+            value(t, u0 + 5 * j + 3, j == 0, lastuse(t, j), j + 1 == nt[t]);
+          if (j + 1 < nt[t] && ok)
+            score(t, u0 + 5 * (j + 1), lastuse(t, j + 1), j + 2 == nt[t]);
+        }
+      u0 += 5 * n;
+    }
+    // everything issued so far has finished before TMEM is released
+    if (elect_one()) tc_commit(&bars.drain);
+    __syncwarp();
+    warp_wait(&bars.drain, 0, nullptr, status);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
+    // ---------------- softmax and output of tile t, thread = token ----------------
+    const int t = warp >> 2, q4 = warp & 3;
+    const int row = q4 * 32 + lane;
+    const uint32_t ts = tmem + ((uint32_t)(q4 * 32) << 16) + t * 128;
+    const uint32_t to = ts - t * 128 + 256 + t * 128;
+    int sn = 0, on = 0;
+    bool ok = true;
+    const uint64_t scale2 = pack2(scale_log2, scale_log2);
+    for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+      const Block b = ly.block[it / heads];
+      const int h = it % heads;
+      const int nt = tiles_of(b, t);
+      const int mine = min(b.n - t * kRows, kRows);  // tokens of this tile
+      if (mine <= 0) continue;
+      const int lim = min(b.kv, b.lim + t * kRows + row);  // positions this token sees
+      const int lim0 = b.lim + t * kRows;                  // ... and the tile's first token
+      float m = -INFINITY;
+      uint64_t l2 = 0;  // two partial row sums
+#pragma unroll 1
+      for (int j = 0; j < nt; ++j) {
+        ok = warp_wait(&bars.s_full[t], sn & 1, abort, status);
+        ++sn;
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, s + c * 32);
+        tc_wait_ld();
+        if (min(b.kv, lim0) < (j + 1) * kRows) {
+          const int left = lim - j * kRows;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c >= left) s[c] = 0xff800000u;
+        }
+        float mx[4] = {u2f(s[0]), u2f(s[1]), u2f(s[2]), u2f(s[3])};
+#pragma unroll
+        for (int c = 4; c < 128; c += 4)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], u2f(s[c + e]));
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
+        const bool raise = mt > m + kRescaleThreshold;
+        if (__any_sync(0xffffffffu, raise)) {
+          // (the value products before these scores have completed with them)
+          const float a = raise ? fast_exp2(m - mt) : 1.f;  // 0 at the first tile
+          if (j > 0) {
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(to + c, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = f2u(u2f(o[e]) * a);
+              tmem_st32(to + c, o);
+            }
+            float x, y;
+            unpack2(l2, x, y);
+            l2 = pack2(x * a, y * a);
+          }
+          if (raise) m = mt;
+        }
+        // (a token that has seen no position yet has m = -inf: its weights are exp2(-inf) = 0)
+        const float d = m == -INFINITY ? 0.f : -m;
+        const uint64_t d2 = pack2(d, d);
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float x, y;
+            unpack2(fma2(pack2(u2f(s[2 * (c + e)]), u2f(s[2 * (c + e) + 1])), scale2, d2), x, y);
+            x = fast_exp2(x);
+            y = fast_exp2(y);
+            l2 = add2(l2, pack2(x, y));
+            w[e] = pack_bf16x2(x, y);
+          }
+          tmem_st32(ts + c, w);
+        }
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full[t]);
+      }
+      if (!ok) break;
+      float inv = 0.f;
+      if (nt > 0) {
+        float x, y;
+        unpack2(l2, x, y);
+        const float l = x + y;
+        inv = l == 0.f ? 0.f : 1.f / l;
+        ok = warp_wait(&bars.o_full[t], on & 1, abort, status);
+        ++on;
+        if (!ok) break;
+        tc_fence_after();
+      }
+      __nv_bfloat16* dst = O + ((size_t)(b.tok + t * kRows + row) * kH + head0 + h) * kD;
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t o[32];
+        if (nt > 0) {
+          tmem_ld32(to + c, o);
+          tc_wait_ld();
+        }
+        if (row < mine) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (lim > 0)
+              v = make_uint4(pack_bf16x2(u2f(o[8 * e]) * inv, u2f(o[8 * e + 1]) * inv),
+                             pack_bf16x2(u2f(o[8 * e + 2]) * inv, u2f(o[8 * e + 3]) * inv),
+                             pack_bf16x2(u2f(o[8 * e + 4]) * inv, u2f(o[8 * e + 5]) * inv),
+                             pack_bf16x2(u2f(o[8 * e + 6]) * inv, u2f(o[8 * e + 7]) * inv));
+            *reinterpret_cast<uint4*>(dst + c + 8 * e) = v;
+          }
+        }
+      }
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ===========================================================================
+// host
+// ===========================================================================
+
+struct Ws {
+  size_t row, kv, block, count, rows, k, v, total;
+  int64_t max_rows;
+  int heads;  // of a group
+};
+
+static Ws layout(int N, int S, int max_kv) {
+  Ws w;
+  // (a pair's second CTA may reach 128 rows past the last sequence)
+  w.max_rows = (int64_t)S * ((max_kv + kRows - 1) / kRows * kRows);
+  w.max_rows = (w.max_rows + 2 * kRows - 1) / (2 * kRows) * (2 * kRows);
+  w.heads = kH;
+  while (w.heads > 8 && (size_t)w.max_rows * w.heads * 2 * kD * 2 > kGroupBytes) w.heads /= 2;
+  w.row = 0;
+  w.kv = round_up((size_t)(S + 1) * 4, 256);
+  w.block = round_up(w.kv + (size_t)S * 4, 256);
+  w.count = round_up(w.block + ((size_t)N / kBlock + S) * sizeof(Block), 256);
+  w.rows = w.count + 256;
+  w.k = round_up(w.rows + (size_t)w.max_rows * MLA_ROW * 2, 256);
+  w.v = w.k + (size_t)w.max_rows * w.heads * kD * 2;
+  w.total = w.v + (size_t)w.max_rows * w.heads * kD * 2;
+  return w;
+}
+
+bool fits(int S, int max_kv) {
+  return (int64_t)S * ((max_kv + kRows - 1) / kRows * kRows) <= kMaxRows;
+}
+
+size_t workspace_bytes(int N, int S, int max_kv) { return layout(N, S, max_kv).total; }
+
 int run(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const mla_bf16_t* wkv_b,
         const paged::Pool& pool, const paged::Seqs& q, float scale, mla_bf16_t* O, uint8_t* ws,
-        int32_t* status, cudaStream_t st) { return MLA_ERR_UNSUPPORTED; }
-}}
+        int32_t* status, cudaStream_t st) {
+  const Ws L = layout(q.N, q.S, q.max_kv);
+  int sms = 0;
+  if (int e = check_device(&sms)) return e;
+  Layout ly;
+  ly.row = reinterpret_cast<int32_t*>(ws + L.row);
+  ly.kv = reinterpret_cast<int32_t*>(ws + L.kv);
+  ly.block = reinterpret_cast<Block*>(ws + L.block);
+  ly.count = reinterpret_cast<int32_t*>(ws + L.count);
+  __nv_bfloat16* rows = reinterpret_cast<__nv_bfloat16*>(ws + L.rows);
+  __nv_bfloat16* k = reinterpret_cast<__nv_bfloat16*>(ws + L.k);
+  __nv_bfloat16* v = reinterpret_cast<__nv_bfloat16*>(ws + L.v);
+  int shift = 0;  // key tiles of a query block into 1024 classes
+  while ((2 * ((q.max_kv + kRows - 1) / kRows) >> shift) > 1023) ++shift;
+  layout_kernel<<<1, 1024, 0, st>>>(q, pool, ly, shift);
+  if (int e = launch_status()) return e;
+  const int64_t want = (L.max_rows + 7) / 8;
+  const int blocks = (int)(want < sms * 32 ? want : sms * 32);
+  if (pool.kind == MLA_PAGE_E4M3)
+    gather_kernel<true><<<blocks, 256, 0, st>>>(pool, ly, q.S, rows, status);
+  else
+    gather_kernel<false><<<blocks, 256, 0, st>>>(pool, ly, q.S, rows, status);
+  if (int e = launch_status()) return e;
+
+  alignas(64) CUtensorMap map_c, map_w, map_k, map_v, map_r, map_qn, map_qr;
+  const uint64_t R = (uint64_t)L.max_rows;
+  if (int e = bf16_map_2d(&map_c, rows, kC, R, MLA_ROW * 2, 64, kRows)) return e;
+  if (int e = bf16_map_2d(&map_w, wkv_b, kC, kH * 256, kC * 2, 64, 128)) return e;
+  if (int e = bf16_map_3d(&map_k, k, kD, R, L.heads, kD * 2, R * kD * 2, 64, kRows, 1)) return e;
+  if (int e = bf16_map_3d(&map_v, v, kD, R, L.heads, kD * 2, R * kD * 2, 64, kRows, 1)) return e;
+  if (int e = bf16_map_2d(&map_r, rows + kC, kR, R, MLA_ROW * 2, 64, kRows)) return e;
+  if (int e = bf16_map_3d(&map_qn, q_nope, kD, kH, q.N, kD * 2, kH * kD * 2, 64, 1, kRows))
+    return e;
+  if (int e = bf16_map_3d(&map_qr, q_pe, kR, kH, q.N, kR * 2, kH * kR * 2, 64, 1, kRows)) return e;
+  static std::atomic<unsigned long long> gemm_attr{0}, attn_attr{0};
+  if (int e = ensure_smem_attr(expand_kernel, gemm::SMEM, &gemm_attr)) return e;
+  if (int e = ensure_smem_attr(chunk_kernel, attn::SMEM, &attn_attr)) return e;
+  for (int h0 = 0; h0 < kH; h0 += L.heads) {
+    expand_kernel<<<2 * (sms / 2), gemm::THREADS, gemm::SMEM, st>>>(
+        map_c, map_w, map_k, map_v, ly.row + q.S, h0, L.heads, status);
+    if (int e = launch_status()) return e;
+    chunk_kernel<<<sms, attn::THREADS, attn::SMEM, st>>>(
+        map_qn, map_qr, map_k, map_r, map_v, ly, h0, L.heads, scale * 1.4426950408889634f,
+        reinterpret_cast<__nv_bfloat16*>(O), status);
+    if (int e = launch_status()) return e;
+  }
+  return MLA_OK;
+}
+
+}  // namespace expand
+}  // namespace shla

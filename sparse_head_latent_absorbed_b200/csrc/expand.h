@@ -8,7 +8,11 @@ namespace expand {
 
 // Average new tokens per sequence from which MLA_FORM_AUTO expands.  By flops
 // alone the forms meet at 33.6e6 / (278,528 - 81,920) = 171 tokens.
-constexpr int kMinTokens = 1 << 20;
+constexpr int kMinTokens = 128;
+
+// Positions of all sequences, each rounded up to 128, that a call may reach.
+constexpr int64_t kMaxRows = 1 << 26;
+bool fits(int S, int max_kv);
 
 size_t workspace_bytes(int N, int S, int max_kv);
 

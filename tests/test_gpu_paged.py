@@ -24,7 +24,7 @@ import paged_ref as R
 pytestmark = pytest.mark.gpu
 
 REL, ELEM = 1e-2, 4e-2
-FORMS = ["absorbed"]
+FORMS = ["absorbed", "expanded"]
 REF = ("q_nope", "q_pe", "wkv_b", "pages", "page_table", "cu_q", "kv_len", "scale")
 
 

@@ -51,7 +51,7 @@ def test_attend(L):
         assert _attend(L, **{k: None}) == -1, k
     for bad in (dict(S=0), dict(N=0), dict(N=65536), dict(S=65536), dict(max_kv=0),
                 dict(max_kv=2 ** 24 + 1), dict(form=3), dict(form=-1), dict(mp=0), dict(P=0),
-                dict(N=65535, max_kv=2 ** 24)):
+                dict(N=65535, max_kv=2 ** 24, form=1), dict(S=2048, max_kv=65536, form=2)):
         assert _attend(L, **bad) == -2, bad
     for k in ("q", "qp", "w", "O", "pool"):
         assert _attend(L, **{k: ODD}) == -3, k
@@ -62,6 +62,18 @@ def test_workspace_sizes(L):
     f = L.mla_attend_paged_workspace_bytes
     assert f(0, 1, 10) == f(1, 0, 10) == f(1, 1, 0) == 0
     # q~ and the mixed latents of each token, two partial ones for each SM pair
-    assert f(16, 16, 100) >= 2 * 16 * 128 * 512 * 2 + 2 * 128 * 512 * 2
+    assert f(16, 16, 100, "absorbed") >= 2 * 16 * 128 * 512 * 2 + 2 * 128 * 512 * 2
+    # keys and values of 128 heads, of fewer where they would pass 4 GiB
+    assert f(128, 1, 128) >= 256 * (1152 + 128 * 512)
+    assert f(512, 1, 2 ** 17) < 2 ** 17 * 1152 + 2 ** 32 + 2 ** 20
+    # the form that "auto" takes
+    assert f(127, 1, 500) == f(127, 1, 500, "absorbed") != f(127, 1, 500, "expanded")
+    assert f(128, 1, 500) == f(128, 1, 500, "expanded")
     with pytest.raises(L.MLAError):
         f(1, 1, 10, "other")
+
+
+def test_scale(L):
+    for s in (0.0, -1.0, float("nan"), float("inf")):
+        assert L.LIB.mla_attend_paged(D, D, D, D, 0, 4, 16, 16 * 1152, 1152, D, 4, D, D, 1, 1, 64,
+                                      s, 0, D, D, 1 << 40, None, None) == -2

@@ -15,6 +15,7 @@
 
 #include "attend_paged.cuh"
 #include "expand.h"
+#include "pair.cuh"
 #include "tma_map.h"
 
 namespace shla {
@@ -109,57 +110,62 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Seqs q, const Pool poo
 }
 
 // ===========================================================================
-// absorbed_kernel: persistent 2-CTA clusters
+// absorbed_kernel: persistent CTA pairs (tcgen05 cta_group::2)
 //
-// One CTA's TMEM cannot hold the 128 x 512 fp32 accumulator of a token's 128
-// heads and anything else, so a pair of CTAs splits the latent: CTA r holds
-// latent columns [256r, 256r+256) and rotary columns [32r, 32r+32) of q~ and
-// of every key.  Per tile of 64 keys:
-//   S_r  = Q~_r K_r^T      M = 128 heads, N = 64, K = 288; A = Q~ in TMEM
-//   the two exchange their fp32 partial scores (st.async into the peer's
-//   shared memory), add them (a + b in one CTA, b + a in the other: the same
-//   numbers) and both run the same fp32 online softmax: running maximum,
-//   raised only once a tile exceeds it by more than 8 log2 units; P = 2^(s-m)
-//   rounded to bf16 as a tensor-core operand (its row sum is of the fp32 P)
-//   O_r += P V_r           M = 128, N = 256, K = 64; A = P in TMEM, V = the
-//   key tile itself, read MN-major
+// A token's fp32 accumulator, 128 heads x 512 latent columns, is a CTA's whole
+// TMEM.  So a pair shares a token: CTA r has heads [64r, +64), whose 64 rows of
+// scores and of output a pair's M = 128 product leaves in its own TMEM, each
+// row in two lanes: lane h the first half of the columns, lane 64 + h the
+// second.  No score ever crosses between the CTAs.  Per tile of 64 keys:
+//   S = Q~ K^T   M = 128, N = 64 keys, K = 576.  A: 64 rows of Q~ in each CTA.
+//                B: CTA r holds keys [32r, +32), all 576 columns.
+//   O += P V     M = 128, N = 2 x 256, K = 64 keys.  A: 64 rows of P in each
+//                CTA.  B: CTA r holds all 64 keys' latent columns [256r, +256),
+//                read MN-major.
+// A row's two lanes hold 32 keys' scores each; they agree on the maximum
+// through shared memory.  fp32 online softmax: the running maximum is raised
+// only once a tile exceeds it by more than 8 log2 units; P = 2^(s-m) is rounded
+// to bf16 as a tensor-core operand (its row sum is of the fp32 P).
 //
-// Roles (640 threads):
-//   warps 0-7    softmax, 16 head rows each, four threads per row: own partial
-//                scores from TMEM + the peer's from shared memory
-//   warps 8-11   senders, one lane quarter each: own partial scores to the
-//                peer; the next token's queries
-//   warps 12-18  keys: TMA boxes of up to 64 rows (16-bit pages; one warp), or
-//                loads, exact conversion to bf16 and swizzled stores (8-bit)
-//   warp 19      TMEM owner and MMA issuer
-// The senders never wait for the peer's scores and the softmax warps never
-// send: the exchange is a pipeline stage, not a round trip.  Scores are
-// double-buffered and P overlays the scores it came from, so the score
-// product of tile i + 1 runs while tile i is in the softmax.
-// TMEM (512 columns): Q~ half [0,128) as bf16 pairs, two score tiles [128,256)
-// (their first 32 columns become P), the output half in fp32 [256,512).
+// Bounds, per tile and pair: 73.7 KB of cache (0.83 us at the measured copy
+// rate for 16-bit pages), 1456 cycles of products (36 x 26 + 8 x 65, measured;
+// 0.76 us at 1.92 GHz).  Keys and values are separate copies with rings of
+// their own (2 x 36 KB, 2 x 32 KB): a key slab is free once its scores are
+// computed, so its reload does not wait for the softmax.  (A pair that splits
+// the latent for scores too holds each value once, but must exchange 32 KB of
+// partial scores a tile; st.async moves them at 23 bytes a cycle and keeps the
+// other shared-memory accesses of the SM waiting: 3600 cycles a tile.)
+//
+// Roles (640 threads a CTA):
+//   warps 0-7    softmax, two groups of four warps that take every other tile, a
+//                lane of TMEM per thread.  The running maximum goes from group
+//                to group (published as soon as a tile's is known, before its
+//                exponentials); row sums stay with the group until the token ends.
+//   warps 8-11   keys; 12-15 values.  16-bit pages: one warp of each, TMA boxes of
+//                up to 64 rows.  8-bit: loads, exact conversion to bf16 and
+//                swizzled stores.
+//   warp 16      MMA issuer (first CTA), TMEM owner
+//   warp 17      queries (TMA)
+// TMEM (512 columns): four score tiles [0,128), output [256,512).
 // ===========================================================================
 
-constexpr int NST = 4;                 // key ring depth
-constexpr int NSOFT = 8;               // softmax warps
-constexpr int SEND_WARP0 = 8;
-constexpr int KEY_WARP0 = 12;
-constexpr int NKEY = 7;
-constexpr int MMA_WARP = 19;
-constexpr int NTHREADS = 32 * (MMA_WARP + 1);
-constexpr int ST_ATOM = KT * 128;      // one 64-column latent atom of a tile (128 B swizzle)
-constexpr int ST_KR = 4 * ST_ATOM;     // rotary half of a tile (64 B swizzle)
-constexpr int ST_BYTES = ST_KR + KT * 64;
-constexpr int OFF_QR = NST * ST_BYTES; // rotary half of Q: 128 rows x 64 B, 64 B swizzle
-constexpr int OFF_XS = OFF_QR + 128 * 64;
-constexpr int XS_BYTES = NSOFT * 8 * 32 * 16;  // the peer's partial scores: [warp][8][32 lanes][16 B]
-constexpr int OFF_ROWSTART = OFF_XS + 2 * XS_BYTES;  // per stage: the tile starts its token
-constexpr int SMEM_BYTES = OFF_ROWSTART + NST * 4 + 1024;  // + alignment slack
-constexpr uint32_t T_Q = 0, T_S = 128, T_O = 256, TMEM_COLS = 512;
+constexpr int HH = kH / 2;             // heads of a CTA
+constexpr int NSB = 4;                 // score tiles in TMEM (32 columns each)
+constexpr int KEY_WARP0 = 8, VAL_WARP0 = 12, MMA_WARP = 16, Q_WARP = 17;
+constexpr int NTHREADS = 640;
+constexpr int Q_ATOM = HH * 128;       // 64 columns of 64 rows, 128 B swizzle
+constexpr int K_ATOM = KT / 2 * 128;   // 64 columns of 32 keys
+constexpr int V_ATOM = KT * 128;       // 64 columns of 64 keys
+constexpr int Q_BYTES = 9 * Q_ATOM, K_BYTES = 9 * K_ATOM, V_BYTES = 4 * V_ATOM;
+constexpr int P_BYTES = HH * 128;      // 64 rows of 64 weights
+constexpr int OFF_K = Q_BYTES;
+constexpr int OFF_V = OFF_K + 2 * K_BYTES;
+constexpr int OFF_P = OFF_V + 2 * V_BYTES;
+constexpr int SMEM_BYTES = OFF_P + 2 * P_BYTES;
+constexpr uint32_t T_S = 0, T_O = 256, TMEM_COLS = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-static_assert(ST_BYTES % 1024 == 0 && OFF_QR % 1024 == 0 && OFF_XS % 16 == 0, "alignment");
-static_assert(SMEM_BYTES + 512 <= 232448, "shared memory budget");
-static_assert(T_Q + 128 <= T_S && T_S + 2 * KT <= T_O && T_O + 256 <= TMEM_COLS, "TMEM plan");
+static_assert(OFF_K % 1024 == 0 && OFF_V % 1024 == 0 && OFF_P % 1024 == 0, "alignment");
+static_assert(T_S + NSB * KT / 2 <= T_O, "TMEM plan");
 
 struct Params {
   const __nv_bfloat16* q_tilde;  // [N][128][512]
@@ -167,7 +173,7 @@ struct Params {
   Pool pool;
   Plan plan;
   int N;
-  int box;                       // rows of a TMA box (16, 32 or 64; 0: row by row)
+  int kbox, vbox;                // rows of a TMA box of keys (16, 32; 0: row by row) and values
   float scale_log2;              // softmax scale * log2(e)
   __nv_bfloat16* opart;          // [pairs][2 slots][128][512], normalised per segment
   float* lse;                    // [pairs][2 slots][128], log2 units of scaled scores
@@ -175,39 +181,34 @@ struct Params {
   int32_t* status;
 };
 
+// "first CTA": waited on by the issuer only, arrived on from both CTAs;
+// "both": committed to both CTAs by the issuer; the others are each CTA's own
 struct Bars {
-  uint64_t full[NST], empty[NST];  // key ring
-  uint64_t s_full[2];              // score tile of tile i in buffer i & 1
-  uint64_t sent[2];                // ... read by the senders
-  uint64_t xs_full[2], xs_free[2]; // the peer's partial scores landed / the peer has read ours
-  uint64_t p_full[2], o_done[2];   // P written over the scores / its value product done
-  uint64_t q_ready;
-  uint64_t drain;
+  uint64_t q_full, q_free;           // first CTA / both
+  uint64_t k_full[2], k_empty[2];    // first CTA / both
+  uint64_t v_full[2], v_empty[2];
+  uint64_t s_full[NSB];              // both: scores of tile i in buffer i % NSB
+  uint64_t p_full[2];                // first CTA: P of tile i in buffer i & 1
+  uint64_t o_done[2];                // both: value product of tile i done
+  uint64_t m_full[2][4];             // running maxima after tile i, by group and lane quarter
+  uint64_t x_full[2][2];             // tile maxima of both lanes of a row (by quarter & 1)
+  uint64_t l_full[2][4];             // row sums after tile i
+  uint64_t flushed[4];               // a token's output has left TMEM, by lane quarter
+  uint64_t drain;                    // both
   uint32_t tmem_base;
   int abort;
+  // by group: running maxima of the heads, tile maxima and row sums of the lanes
+  float m[2][HH], x[2][128], l[2][128];
 };
 
-// one lane of a converged warp, the same every time
-DEV bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(p));
-  return p != 0;
-}
+static_assert((sizeof(Bars) + 1023) / 1024 * 1024 + SMEM_BYTES <= 232448,
+              "shared memory budget");
 
-// D[tmem] (+)= A[tmem] * B[smem]^T, the accumulate flag at run time
-DEV void tc_mma_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                       uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+// Dynamic shared memory: the operands from the first 1024-byte boundary after
+// the kernel's static part, which is Bars.
+static constexpr int dynamic_smem() {
+  return SMEM_BYTES + (1024 - (int)(sizeof(Bars) % 1024)) % 1024;
 }
-
-DEV float u2f(uint32_t x) { return __uint_as_float(x); }
-DEV uint32_t f2u(float x) { return __float_as_uint(x); }
 
 struct Pos {
   int bb, jt, nr;  // token, tile within it, its tile count
@@ -215,17 +216,22 @@ struct Pos {
 
 template <bool kE4M3>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
-    absorbed_kernel(const Params p, const __grid_constant__ CUtensorMap map_c,
-                    const __grid_constant__ CUtensorMap map_r,
-                    const __grid_constant__ CUtensorMap map_c1,
-                    const __grid_constant__ CUtensorMap map_r1) {
+    absorbed_kernel(const Params p, const __grid_constant__ CUtensorMap map_qt,
+                    const __grid_constant__ CUtensorMap map_qr,
+                    const __grid_constant__ CUtensorMap map_k,
+                    const __grid_constant__ CUtensorMap map_v,
+                    const __grid_constant__ CUtensorMap map_1) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   __shared__ Bars bars;
   volatile int* abort = &bars.abort;
 
+  // (the static part begins on such a boundary; were it not so, nothing runs)
+  if (smem + SMEM_BYTES > smem_raw + dynamic_smem()) {
+    report_timeout(p.status);
+    return;
+  }
   const uint32_t rank = cluster_ctarank();
-  const uint32_t peer = rank ^ 1u;
   const int cid = blockIdx.x >> 1;
   // (the plan was complete before the fold kernel began)
   const int t_begin = ld_global_nc_s32_early(p.plan.tb + cid);
@@ -242,29 +248,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     : 1;
   };
   auto lim_of = [&](int bb) { return bb < p.N ? ld_global_nc_s32_early(p.plan.lim + bb) : 0; };
+  // a barrier of the pair's first CTA
+  auto first_cta = [&](uint64_t* bar) { return mapa_shared(smem_u32(bar), 0); };
 
-  if (warp == MMA_WARP) {
-    tmem_alloc(&bars.tmem_base, TMEM_COLS);
-    tmem_relinquish();
-  }
+  if (warp == MMA_WARP) tmem_alloc2(&bars.tmem_base, TMEM_COLS);
   if (tid == 0) {
-    for (int s = 0; s < NST; ++s) {
-      mbar_init(&bars.full[s], kE4M3 ? NKEY : 1);
-      mbar_init(&bars.empty[s], 1);
-    }
+    constexpr int fill = kE4M3 ? 8 : 1;  // four warps of each CTA, or one arrival and bytes
+    mbar_init(&bars.q_full, 1);
+    mbar_init(&bars.q_free, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.s_full[i], 1);
-      mbar_init(&bars.sent[i], 4);
-      mbar_init(&bars.xs_full[i], 1);      // own expect_tx arrival + the peer's bytes
-      mbar_init(&bars.xs_free[i], NSOFT);  // one arrival per softmax warp of the peer
-      mbar_init(&bars.p_full[i], NSOFT);
+      mbar_init(&bars.k_full[i], fill);
+      mbar_init(&bars.v_full[i], fill);
+      mbar_init(&bars.k_empty[i], 1);
+      mbar_init(&bars.v_empty[i], 1);
+      mbar_init(&bars.p_full[i], 8);
       mbar_init(&bars.o_done[i], 1);
+      mbar_init(&bars.x_full[i][0], 2);
+      mbar_init(&bars.x_full[i][1], 2);
+      for (int q = 0; q < 4; ++q) {
+        mbar_init(&bars.m_full[i][q], 1);
+        mbar_init(&bars.l_full[i][q], 1);
+      }
     }
-    mbar_init(&bars.q_ready, 4);
+    for (int i = 0; i < NSB; ++i) mbar_init(&bars.s_full[i], 1);
+    for (int q = 0; q < 4; ++q) mbar_init(&bars.flushed[q], 1);
     mbar_init(&bars.drain, 1);
     bars.abort = 0;
     fence_mbarrier_init_cluster();
-    for (int i = 0; i < 2 && i < n; ++i) mbar_arrive_expect_tx(&bars.xs_full[i], XS_BYTES);
   }
   tc_fence_before();
   cluster_sync_all();
@@ -274,10 +284,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   if (n <= 0) {
     // an empty range (fewer tiles than pairs): nothing to do
   } else if (warp >= KEY_WARP0 && warp < MMA_WARP) {
-    // ---------------- keys ----------------
-    const int kw = warp - KEY_WARP0;
-    if (kE4M3 || kw == 0) {
-      int bb = bb0, jt = jt0 - 1, nr = tiles_of(bb0), lim = 0, issued = 0, bad = 0;
+    // ---------------- keys and values ----------------
+    const bool val = warp >= VAL_WARP0;
+    const int w4 = warp & 3;
+    uint64_t* full = val ? bars.v_full : bars.k_full;
+    uint64_t* empty = val ? bars.v_empty : bars.k_empty;
+    const uint32_t full0 = first_cta(full);
+    if (kE4M3 || w4 == 0) {
+      // this CTA's rows of a tile: 32 keys, or all 64 for values.  Lane l holds
+      // the pool rows of the l-th and (values) the (32 + l)-th.
+      const int sub = val ? 0 : rank * 32;
+      int bb = bb0, jt = jt0 - 1, nr = tiles_of(bb0), lim = 0, bad = 0;
       const int32_t* trow = nullptr;
       bool last = false;  // the token sees all its sequence's positions: count its bad pages
       auto enter = [&]() {
@@ -289,546 +306,470 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                ld_global_nc_s32_early(p.plan.seq + bb + 1) != s;
       };
       enter();
-      int ra = 0, rb = 0, key0 = 0;  // rows of keys lane and 32 + lane of the current tile
-      bool start = false;
+      int ra = 0, rb = 0, key0 = 0;
       auto next_tile = [&]() {
         if (++jt == nr) {
           jt = 0;
           nr = tiles_of(++bb);
           enter();
         }
-        key0 = jt * KT;
-        start = jt == 0;
+        key0 = jt * KT + sub;
         ra = rb = p.pool.rows;
         if (key0 + lane < lim) ra = row_of(p.pool, trow, key0 + lane);
-        if (key0 + 32 + lane < lim) rb = row_of(p.pool, trow, key0 + 32 + lane);
-      };
-      // entries outside the pool, each page of a sequence once
-      auto count_bad = [&]() {
-        if (rank == 0 && kw == 0 && last) {
+        if (val && key0 + 32 + lane < lim) rb = row_of(p.pool, trow, key0 + 32 + lane);
+        // entries outside the pool, each page of a sequence once
+        if (val && rank == 0 && w4 == 0 && last) {
           const int a = key0 + lane, b = a + 32;
           bad += a < lim && ra == p.pool.rows && a % p.pool.page_size == 0;
           bad += b < lim && rb == p.pool.rows && b % p.pool.page_size == 0;
         }
       };
+      // the pool row of the tile's row k (whole warp)
+      auto row = [&](int k) {
+        const int ya = __shfl_sync(0xffffffffu, ra, k & 31);
+        const int yb = __shfl_sync(0xffffffffu, rb, k & 31);
+        return k < 32 ? ya : yb;
+      };
+      next_tile();
       if constexpr (!kE4M3) {
-        next_tile();
+        const int rows = val ? KT : KT / 2, box = val ? p.vbox : p.kbox;
+        const int atoms = val ? 4 : 9, x0 = val ? rank * 256 : 0;
+        const int bytes = val ? V_BYTES : K_BYTES, atom_bytes = rows * 128;
+        const CUtensorMap* map = val ? &map_v : &map_k;
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
-          const int s = i % NST;
-          count_bad();
-          const int xa = ra, xb = rb;
-          const bool boxes = p.box && key0 + KT <= lim;
-          const uint32_t st_start = i == 0 || start ? 1u : 0u;
-          if (i + 1 < n) next_tile();
-          if (!warp_wait(&bars.empty[s], ((i / NST) & 1) ^ 1, abort, p.status)) break;
-          if (lane == 0) {
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(sbase + OFF_ROWSTART + s * 4),
-                         "r"(st_start)
-                         : "memory");
-            mbar_arrive_expect_tx(&bars.full[s], ST_BYTES);
-          }
-          __syncwarp();
-          const uint32_t stage = sbase + s * ST_BYTES;
+          const int s = i & 1;
+          const bool boxes = box && key0 + rows <= lim;
+          int y[4];
+          int k0;
           if (boxes) {
             // whole boxes of rows: every page boundary is a box boundary
-            const int k0 = (lane * p.box) & 63;
-            const int ya = __shfl_sync(0xffffffffu, xa, k0 & 31);
-            const int yb = __shfl_sync(0xffffffffu, xb, k0 & 31);
-            const int y = k0 < 32 ? ya : yb;
-            if (lane * p.box < KT) {
-#pragma unroll
-              for (int a = 0; a < 4; ++a)
-                tma_load_2d(stage + a * ST_ATOM + k0 * 128, &map_c, rank * 256 + a * 64, y,
-                            &bars.full[s]);
-              tma_load_2d(stage + ST_KR + k0 * 64, &map_r, rank * 32, y, &bars.full[s]);
-            }
+            k0 = (lane * box) & (rows - 1);
+            y[0] = row(k0);
           } else {
             // row by row: the tile's rows past the limit read as zeros, so
             // that nothing stored there can reach a product
-            const int k0 = 4 * (lane & 15), src = k0 & 31;
-            int y[4];
+            k0 = (4 * lane) & (rows - 1);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int ya = __shfl_sync(0xffffffffu, xa, src + j);
-              const int yb = __shfl_sync(0xffffffffu, xb, src + j);
-              y[j] = k0 < 32 ? ya : yb;
-            }
-            if (lane < 16) {
-#pragma unroll
-              for (int a = 0; a < 4; ++a)
-                tma_gather4(stage + a * ST_ATOM + k0 * 128, &map_c1, rank * 256 + a * 64, y[0],
-                            y[1], y[2], y[3], &bars.full[s]);
-              tma_gather4(stage + ST_KR + k0 * 64, &map_r1, rank * 32, y[0], y[1], y[2], y[3],
-                          &bars.full[s]);
-            }
+            for (int j = 0; j < 4; ++j) y[j] = row(k0 + j);
           }
-          issued = i + 1;
+          if (i + 1 < n) next_tile();
+          if (!warp_wait(&empty[s], ((i >> 1) & 1) ^ 1, abort, p.status)) break;
+          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
+          __syncwarp();
+          const uint32_t slab = sbase + (val ? OFF_V : OFF_K) + s * bytes;
+          const uint32_t bar = full0 + s * 8;
+          if (boxes) {
+            if (lane * box < rows)
+              for (int a = 0; a < atoms; ++a)
+                tma_load_2d_pair(slab + a * atom_bytes + k0 * 128, map, x0 + a * 64, y[0], bar);
+          } else if (lane * 4 < rows) {
+            for (int a = 0; a < atoms; ++a)
+              tma_gather4_pair(slab + a * atom_bytes + k0 * 128, &map_1, x0 + a * 64, y[0], y[1],
+                               y[2], y[3], bar);
+          }
         }
-        // on an abort, the loads still in flight land before the CTA can leave
-        for (int t = max(0, issued - NST); t < issued; ++t)
-          warp_wait(&bars.full[t % NST], (t / NST) & 1, nullptr, nullptr);
-      } else {
-        // two rows per warp and step: lane = (row of the pair, 16-code chunk)
-        constexpr int STEPS = (KT / 2 + NKEY - 1) / NKEY;
-        const int rsel = lane >> 4, ch = lane & 15;
-        uint4 code[STEPS], rope[2];
-        float sc[STEPS];
+      } else if (!val) {
+        // 8-bit keys: a row per step and warp, 16 codes per lane
+        uint4 code[8], rope[2];
+        float sc[8];
         auto load = [&]() {
 #pragma unroll
-          for (int it = 0; it < STEPS; ++it) {
-            const int row = 2 * (kw + NKEY * it) + rsel;
-            const int ya = __shfl_sync(0xffffffffu, ra, row & 31);
-            const int yb = __shfl_sync(0xffffffffu, rb, row & 31);
-            const int y = row < 32 ? ya : yb;
+          for (int it = 0; it < 8; ++it) {
+            const int y = row(w4 * 8 + it);
             code[it] = make_uint4(0, 0, 0, 0);
             sc[it] = 1.f;
-            if (row < KT && y < p.pool.rows) {
+            if (y < p.pool.rows) {
+              const uint8_t* src = p.pool.base + (long long)y * p.pool.row_stride;
+              code[it] = ld_global_nc_v4(src + lane * 16);
+              sc[it] = u2f((uint32_t)ld_global_nc_s32_early(
+                  reinterpret_cast<const int32_t*>(src + pages::kScaleOff + (lane >> 3) * 4)));
+            }
+          }
+#pragma unroll
+          for (int it = 0; it < 2; ++it) {
+            const int y = row(w4 * 8 + it * 4 + (lane >> 3));
+            rope[it] = make_uint4(0, 0, 0, 0);
+            if (y < p.pool.rows)
+              rope[it] = ld_global_nc_v4(p.pool.base + (long long)y * p.pool.row_stride +
+                                         pages::kRopeOff + (lane & 7) * 16);
+          }
+        };
+        load();
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+          const int s = i & 1;
+          if (i + 1 < n) next_tile();
+          if (!warp_wait(&empty[s], ((i >> 1) & 1) ^ 1, abort, p.status)) break;
+          const uint32_t slab = sbase + OFF_K + s * K_BYTES;
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            const int r = w4 * 8 + it, c = (lane & 3) * 2;
+            const uint32_t atom = slab + (lane >> 2) * K_ATOM;
+            uint4 o0, o1;
+            pages::dequant16(code[it], sc[it], o0, o1);
+            st_shared_v4(atom + sw128_off(r, c), o0.x, o0.y, o0.z, o0.w);
+            st_shared_v4(atom + sw128_off(r, c + 1), o1.x, o1.y, o1.z, o1.w);
+          }
+#pragma unroll
+          for (int it = 0; it < 2; ++it)
+            st_shared_v4(slab + 8 * K_ATOM + sw128_off(w4 * 8 + it * 4 + (lane >> 3), lane & 7),
+                         rope[it].x, rope[it].y, rope[it].z, rope[it].w);
+          if (i + 1 < n) load();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(full0 + s * 8);
+        }
+      } else {
+        // 8-bit values: two rows per step and warp, 16 codes per lane
+        const int rsel = lane >> 4, ch = lane & 15;
+        uint4 code[8];
+        float sc[8];
+        auto load = [&]() {
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            const int y = row(w4 * 16 + it * 2 + rsel);
+            code[it] = make_uint4(0, 0, 0, 0);
+            sc[it] = 1.f;
+            if (y < p.pool.rows) {
               const uint8_t* src = p.pool.base + (long long)y * p.pool.row_stride;
               code[it] = ld_global_nc_v4(src + rank * 256 + ch * 16);
               sc[it] = u2f((uint32_t)ld_global_nc_s32_early(reinterpret_cast<const int32_t*>(
                   src + pages::kScaleOff + (rank * 2 + (ch >> 3)) * 4)));
             }
           }
-#pragma unroll
-          for (int it = 0; it < 2; ++it) {
-            const int u = kw * 32 + lane + it * NKEY * 32;  // (row, 16-byte chunk) of the rotary half
-            const int row = (u >> 2) & 63;
-            const int ya = __shfl_sync(0xffffffffu, ra, row & 31);
-            const int yb = __shfl_sync(0xffffffffu, rb, row & 31);
-            const int y = row < 32 ? ya : yb;
-            rope[it] = make_uint4(0, 0, 0, 0);
-            if (u < KT * 4 && y < p.pool.rows)
-              rope[it] = ld_global_nc_v4(p.pool.base + (long long)y * p.pool.row_stride +
-                                         pages::kRopeOff + rank * 64 + (u & 3) * 16);
-          }
         };
-        next_tile();
         load();
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
-          const int s = i % NST;
-          count_bad();
-          const uint32_t st_start = i == 0 || start ? 1u : 0u;
+          const int s = i & 1;
           if (i + 1 < n) next_tile();
-          if (!warp_wait(&bars.empty[s], ((i / NST) & 1) ^ 1, abort, p.status)) break;
-          const uint32_t stage = sbase + s * ST_BYTES;
-          if (kw == 0 && lane == 0)
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(sbase + OFF_ROWSTART + s * 4),
-                         "r"(st_start)
-                         : "memory");
+          if (!warp_wait(&empty[s], ((i >> 1) & 1) ^ 1, abort, p.status)) break;
+          const uint32_t slab = sbase + OFF_V + s * V_BYTES;
 #pragma unroll
-          for (int it = 0; it < STEPS; ++it) {
-            const int row = 2 * (kw + NKEY * it) + rsel;
-            if (row >= KT) continue;
+          for (int it = 0; it < 8; ++it) {
+            const int r = w4 * 16 + it * 2 + rsel, c = (ch & 3) * 2;
+            const uint32_t atom = slab + (ch >> 2) * V_ATOM;
             uint4 o0, o1;
             pages::dequant16(code[it], sc[it], o0, o1);
-            const uint32_t atom = stage + (ch >> 2) * ST_ATOM;
-            const int c2 = (ch & 3) * 2;
-            st_shared_v4(atom + sw128_off(row, c2), o0.x, o0.y, o0.z, o0.w);
-            st_shared_v4(atom + sw128_off(row, c2 + 1), o1.x, o1.y, o1.z, o1.w);
-          }
-#pragma unroll
-          for (int it = 0; it < 2; ++it) {
-            const int u = kw * 32 + lane + it * NKEY * 32;
-            if (u < KT * 4)
-              st_shared_v4(stage + ST_KR + sw64_off(u >> 2, u & 3), rope[it].x, rope[it].y,
-                           rope[it].z, rope[it].w);
+            st_shared_v4(atom + sw128_off(r, c), o0.x, o0.y, o0.z, o0.w);
+            st_shared_v4(atom + sw128_off(r, c + 1), o1.x, o1.y, o1.z, o1.w);
           }
           if (i + 1 < n) load();
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.full[s]);
+          if (lane == 0) mbar_arrive_cluster(full0 + s * 8);
         }
       }
       bad = __reduce_add_sync(0xffffffffu, bad);
       if (lane == 0 && bad && p.status) atomicAdd(p.status + 1, bad);
     }
+  } else if (warp == Q_WARP) {
+    // ---------------- queries: this CTA's 64 heads of each token ----------------
+    pdl_wait();  // q~ is the fold kernel's output (the other roles read only inputs and the plan)
+    const uint32_t bar = first_cta(&bars.q_full);
+    int bb = bb0, i = 0;
+    for (int seg = 0; i < n; ++seg, ++bb) {
+      if (!warp_wait(&bars.q_free, (seg & 1) ^ 1, abort, p.status)) break;
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive_expect_tx(&bars.q_full, 2 * Q_BYTES);
+        for (int a = 0; a < 8; ++a)
+          tma_load_3d_pair(sbase + a * Q_ATOM, &map_qt, a * 64, rank * HH, bb, bar);
+        tma_load_3d_pair(sbase + 8 * Q_ATOM, &map_qr, 0, rank * HH, bb, bar);
+      }
+      __syncwarp();
+      i += tiles_of(bb) - (seg == 0 ? jt0 : 0);
+    }
   } else if (warp == MMA_WARP) {
     // ---------------- MMA issuer ----------------
-    // A value product goes first whenever its P is ready; the score product of
-    // tile i + 2 follows the value product of tile i, whose P it overwrites
-    // (products of one thread run in the order they are issued).  The whole
-    // warp runs the loop and an elected lane issues: under elect.sync the
-    // compiler keeps descriptors in uniform registers, 20 cycles an issue
-    // against 50 from a branch on the lane number, which was more than the 32
-    // cycles such a product takes.
-    constexpr uint32_t idesc_qk = idesc_bf16_f32(128, KT, 0, 0);
-    constexpr uint32_t idesc_pv = idesc_bf16_f32(128, 256, 0, 1);
-    constexpr uint32_t hi_k128 = desc_hi(1024, kSwizzle128B);
-    constexpr uint32_t hi_k64 = desc_hi(512, kSwizzle64B);
-    const uint32_t lo_qr = desc_lo(sbase + OFF_QR, 16);
-    auto test = [](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0;
-    };
-    int qk = 0, pv = 0, idle = 0, qseg = -1;
-    int qs = 0, qph = 0, ps = 0;
-    uint64_t t_idle = 0;
+    // A value product goes first whenever its P is ready, then the score
+    // product of a tile whose keys have landed and whose buffer's earlier
+    // scores both CTAs have turned into a P.
+    if (rank == 0) {
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, KT, 0, 0);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, 256, 0, 1);
+      constexpr uint32_t hi128 = desc_hi(1024, kSwizzle128B);
+      const uint32_t lo_q = desc_lo(sbase, 16);
+      auto test = [](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_test_cluster(bar, parity)) != 0;
+      };
+      Pos cq = {bb0, jt0, tiles_of(bb0)}, cv = cq;  // tiles of the next score / value product
+      int qk = 0, pv = 0, idle = 0, seg = 0;
+      uint64_t t_idle = 0;
 #pragma unroll 1
-    while (pv < n) {
-      bool did = false;
-      if (pv < qk && test(&bars.p_full[pv & 1], (pv >> 1) & 1)) {
-        tc_fence_after();
-        const uint32_t lo = desc_lo(sbase + ps * ST_BYTES, ST_ATOM);  // V, MN-major
-        const uint32_t tp = tmem + T_S + (pv & 1) * KT;
-        const uint32_t first = ld_shared_u32(sbase + OFF_ROWSTART + ps * 4);
-        if (elect_one()) {
-          tc_mma_tmem_a(tmem + T_O, tp, desc_join(lo, hi_k128), idesc_pv, first ^ 1u);
-#pragma unroll
-          for (int ks = 1; ks < KT / 16; ++ks)
-            tc_mma_tmem_a_c<true>(tmem + T_O, tp + ks * 8,
-                                  desc_join(lo + ks * (2048 >> 4), hi_k128), idesc_pv);
-          tc_commit(&bars.o_done[pv & 1]);
-          tc_commit(&bars.empty[ps]);
-        }
-        __syncwarp();
-        ++pv;
-        if (++ps == NST) ps = 0;
-        did = true;
-      }
-      if (qk < n && qk < pv + 2 && test(&bars.full[qs], qph)) {
-        const int seg = ld_shared_u32(sbase + OFF_ROWSTART + qs * 4) ? qseg + 1 : qseg;
-        if (seg == qseg || test(&bars.q_ready, seg & 1)) {
-          qseg = seg;
+      while (pv < n) {
+        bool did = false;
+        if (pv < qk && test(&bars.p_full[pv & 1], (pv >> 1) & 1) &&
+            test(&bars.v_full[pv & 1], (pv >> 1) & 1)) {
           tc_fence_after();
-          const uint32_t st = sbase + qs * ST_BYTES;
-          const uint32_t lo = desc_lo(st, 16), lo_r = desc_lo(st + ST_KR, 16);
-          const uint32_t ts = tmem + T_S + (qk & 1) * KT;
+          const uint32_t lo_v = desc_lo(sbase + OFF_V + (pv & 1) * V_BYTES, V_ATOM);  // MN-major
+          const uint32_t lo_p = desc_lo(sbase + OFF_P + (pv & 1) * P_BYTES, 16);
+          const uint32_t first = pv == 0 || cv.jt == 0 ? 1u : 0u;
           if (elect_one()) {
-            tc_mma_tmem_a_c<false>(ts, tmem + T_Q, desc_join(lo, hi_k128), idesc_qk);
 #pragma unroll
-            for (int ks = 1; ks < 16; ++ks)
-              tc_mma_tmem_a_c<true>(
-                  ts, tmem + T_Q + ks * 8,
-                  desc_join(lo + (((ks >> 2) * ST_ATOM + (ks & 3) * 32) >> 4), hi_k128), idesc_qk);
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-              tc_mma_c<true>(ts, desc_join(lo_qr + ks * 2, hi_k64),
-                             desc_join(lo_r + ks * 2, hi_k64), idesc_qk);
-            tc_commit(&bars.s_full[qk & 1]);
+              for (int ks = 0; ks < KT / 16; ++ks)
+                tc_mma2(tmem + T_O + j * 128, desc_join(lo_p + ks * 2, hi128),
+                        desc_join(lo_v + ((j * 2 * V_ATOM + ks * 2048) >> 4), hi128), idesc_pv,
+                        ks > 0 ? 1u : first ^ 1u);
+            tc_commit2(&bars.o_done[pv & 1]);
+            tc_commit2(&bars.v_empty[pv & 1]);
           }
           __syncwarp();
-          ++qk;
-          if (++qs == NST) {
-            qs = 0;
-            qph ^= 1;
+          ++pv;
+          if (++cv.jt == cv.nr) {
+            cv.jt = 0;
+            cv.nr = tiles_of(++cv.bb);
           }
           did = true;
         }
-      }
-      if (did) {
-        idle = 0;
-        t_idle = 0;
-      } else if (++idle >= 64) {
-        idle = 0;
-        if (__any_sync(0xffffffffu, *abort != 0)) break;
-        const uint64_t now = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
-        if (t_idle == 0) {
-          t_idle = now;
-        } else if (now - t_idle > kWaitLimitNs) {
-          if (lane == 0) {
-            *abort = 1;
-            report_timeout(p.status);
+        if (qk < n && qk < pv + NSB && test(&bars.k_full[qk & 1], (qk >> 1) & 1) &&
+            test(&bars.q_full, seg & 1)) {
+          tc_fence_after();
+          const uint32_t lo_k = desc_lo(sbase + OFF_K + (qk & 1) * K_BYTES, 16);
+          const uint32_t ts = tmem + T_S + (qk % NSB) * (KT / 2);
+          const bool ends = cq.jt == cq.nr - 1;
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < 36; ++ks)
+              tc_mma2(ts, desc_join(lo_q + (((ks >> 2) * Q_ATOM + (ks & 3) * 32) >> 4), hi128),
+                      desc_join(lo_k + (((ks >> 2) * K_ATOM + (ks & 3) * 32) >> 4), hi128),
+                      idesc_qk, ks > 0 ? 1u : 0u);
+            tc_commit2(&bars.s_full[qk % NSB]);
+            tc_commit2(&bars.k_empty[qk & 1]);
+            if (ends) tc_commit2(&bars.q_free);
           }
-          break;
+          __syncwarp();
+          ++qk;
+          if (++cq.jt == cq.nr) {
+            cq.jt = 0;
+            cq.nr = tiles_of(++cq.bb);
+            ++seg;
+          }
+          did = true;
+        }
+        if (did) {
+          idle = 0;
+          t_idle = 0;
+        } else if (++idle >= 64) {
+          idle = 0;
+          if (__any_sync(0xffffffffu, *abort != 0)) break;
+          const uint64_t now = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
+          if (t_idle == 0) {
+            t_idle = now;
+          } else if (now - t_idle > kWaitLimitNs) {
+            if (lane == 0) {
+              *abort = 1;
+              report_timeout(p.status);
+            }
+            break;
+          }
         }
       }
-    }
-    // everything issued so far has finished before TMEM is released
-    if (elect_one()) tc_commit(&bars.drain);
-    __syncwarp();
-    warp_wait(&bars.drain, 0, nullptr, p.status);
-  } else if (warp >= SEND_WARP0) {
-    // ---------------- senders ----------------
-    // Lane quarter q as two 16-lane halves in the 16x256b fragment order of
-    // softmax warps q and q + 4: register 4k + e of half hf is 16-byte chunk k
-    // of softmax warp q + 4 hf.
-    const int q4 = warp - SEND_WARP0;
-    const uint32_t xs_peer = mapa_shared(sbase + OFF_XS + lane * 16, peer);
-    const uint32_t xs_full_peer = mapa_shared(smem_u32(&bars.xs_full[0]), peer);
-    // the quarter's 32 rows of this CTA's half of Q~ for token bb (one row
-    // per thread): latent values into TMEM as bf16 pairs, rotary values into
-    // the swizzled shared tile
-    auto load_q = [&](int bb) {
-      const int h = q4 * 32 + lane;
-      const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
-      const __nv_bfloat16* qrow = p.q_tilde + ((size_t)bb * kH + h) * kC + rank * 256;
-#pragma unroll 1
-      for (int c = 0; c < 4; c += 2) {
-        uint4 v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = ld_global_nc_v4(qrow + c * 64 + i * 8);
-#pragma unroll
-        for (int hc = 0; hc < 2; ++hc) {
-          uint32_t r[32];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            r[4 * i] = v[8 * hc + i].x;
-            r[4 * i + 1] = v[8 * hc + i].y;
-            r[4 * i + 2] = v[8 * hc + i].z;
-            r[4 * i + 3] = v[8 * hc + i].w;
-          }
-          tmem_st32(tmem + lane_base + T_Q + (c + hc) * 32, r);
-        }
-      }
-      const __nv_bfloat16* rrow = p.q_pe + ((size_t)bb * kH + h) * kR + rank * 32;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint4 v = ld_global_nc_v4(rrow + c * 8);
-        st_shared_v4(sbase + OFF_QR + sw64_off(h, c), v.x, v.y, v.z, v.w);
-      }
-      fence_proxy_async_smem();
-      tc_wait_st();
-      tc_fence_before();
+      // everything issued so far has finished before TMEM is released
+      if (elect_one()) tc_commit2(&bars.drain);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.q_ready);
-    };
-    // this thread's part of the next token's queries into L2, a token ahead
-    auto prefetch_q = [&](int i, const Pos& c) {
-      if (i + c.nr - c.jt >= n) return;
-      const int h = q4 * 32 + lane;
-      const __nv_bfloat16* qrow = p.q_tilde + ((size_t)(c.bb + 1) * kH + h) * kC + rank * 256;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) prefetch_l2(qrow + j * 64);
-      prefetch_l2(p.q_pe + ((size_t)(c.bb + 1) * kH + h) * kR + rank * 32);
-    };
-    pdl_wait();  // q~ is the fold kernel's output (the other roles read only inputs and the plan)
-    load_q(bb0);
-    Pos c = {bb0, jt0, tiles_of(bb0)};
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-      const int b = i & 1, ph = (i >> 1) & 1;
-      if (i == 0 || c.jt == 0) prefetch_q(i, c);
-      if (!warp_wait(&bars.s_full[b], ph, abort, p.status)) break;
-      tc_fence_after();
-      uint32_t r[2][32];
-      tmem_ld_16x256b_x8(tmem + ((uint32_t)(q4 * 32) << 16) + T_S + b * KT, r[0]);
-      tmem_ld_16x256b_x8(tmem + ((uint32_t)(q4 * 32 + 16) << 16) + T_S + b * KT, r[1]);
-      tc_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      // relaxed: the tcgen05 loads have completed (waited for above)
-      if (lane == 0) mbar_arrive_relaxed(&bars.sent[b]);
-      // the peer has read its buffer of tile i - 2
-      if (!warp_wait<true>(&bars.xs_free[b], ph ^ 1, abort, p.status)) break;
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          st_async_u4(xs_peer + b * XS_BYTES + (q4 + 4 * hf) * 4096 + k * 512, r[hf][4 * k],
-                      r[hf][4 * k + 1], r[hf][4 * k + 2], r[hf][4 * k + 3],
-                      xs_full_peer + b * 8);
-      // the token's last score product is done: its queries make room for the
-      // next token's
-      if (c.jt == c.nr - 1 && i + 1 < n) load_q(c.bb + 1);
-      if (++c.jt == c.nr) {
-        c.jt = 0;
-        c.nr = tiles_of(++c.bb);
-      }
+      warp_wait<true>(&bars.drain, 0, nullptr, p.status);
     }
-  } else {
-    // ---------------- softmax: rows [32q + 16h, +16), all keys ----------------
-    // Through the 16x256b TMEM shape thread t holds rows t/4 and t/4 + 8 of
-    // its 16 and, of each 8-key block j, keys 8j + 2(t%4) and 8j + 2(t%4) + 1:
-    // register 4j+e is (row t/4 + 8 (e/2), key 8j + 2(t%4) + e%2).
-    const int q4 = warp & 3, hf = warp >> 2;
-    const int c4 = lane & 3;
-    const int row0 = q4 * 32 + hf * 16 + (lane >> 2), row1 = row0 + 8;
-    const uint32_t frag = (uint32_t)(q4 * 32 + hf * 16) << 16;
-    const uint32_t xs_own = sbase + OFF_XS + warp * 4096 + lane * 16;
-    const uint32_t xs_free_peer = mapa_shared(smem_u32(&bars.xs_free[0]), peer);
-    bool alive = true;
-
+  } else if (warp < KEY_WARP0) {
+    // ---------------- softmax: group g = tiles i with i % 2 == g ----------------
+    // Thread = TMEM lane: head h = lane % 64 of this CTA's, keys (and latent
+    // columns) of half lane / 64.
+    const int g = warp >> 2, q4 = warp & 3;
+    const int ln = q4 * 32 + lane, h = ln & 63, half = ln >> 6;
+    const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
+    const uint32_t to = tmem + lane_base + T_O;
+    const uint32_t p_row = sbase + OFF_P + g * P_BYTES;
+    const uint32_t p_bar = first_cta(&bars.p_full[g]);
     auto wait_pv = [&](int t) -> bool {  // the value product of tile t has completed
-      if (!warp_wait(&bars.o_done[t & 1], (t >> 1) & 1, abort, p.status)) return false;
+      if (!warp_wait<true>(&bars.o_done[t & 1], (t >> 1) & 1, abort, p.status)) return false;
       tc_fence_after();
       return true;
     };
-    auto rescale_o = [&](float a0, float a1) {
-#pragma unroll 1
-      for (int cc = 0; cc < 256; cc += 32) {
-        uint32_t r[16];
-        const uint32_t ta = tmem + frag + T_O + cc;
-        tmem_ld_16x256b_x4(ta, r);
-        tc_wait_ld();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          r[4 * j] = f2u(u2f(r[4 * j]) * a0);
-          r[4 * j + 1] = f2u(u2f(r[4 * j + 1]) * a0);
-          r[4 * j + 2] = f2u(u2f(r[4 * j + 2]) * a1);
-          r[4 * j + 3] = f2u(u2f(r[4 * j + 3]) * a1);
-        }
-        tmem_st_16x256b_x4(ta, r);
-      }
-      tc_wait_st();
-    };
-    float m0 = -INFINITY, m1 = -INFINITY;  // running maxima of the two rows (log2 units)
-    float l0 = 0.f, l1 = 0.f;              // this thread's parts of their row sums
-    // A segment's end: this thread's rows of this CTA's half of O~ / l into the
-    // token's output (a token held whole by this pair), or rounded to bf16 into
-    // the pair's slot (0: the range's first segment, 1: its last) with the
-    // segment's log-sum-exps
-    auto flush = [&](int i_last, int bb, bool partial, int slot1) -> bool {
-      float t0 = l0 + __shfl_xor_sync(0xffffffffu, l0, 1);
-      t0 += __shfl_xor_sync(0xffffffffu, t0, 2);
-      float t1 = l1 + __shfl_xor_sync(0xffffffffu, l1, 1);
-      t1 += __shfl_xor_sync(0xffffffffu, t1, 2);
-      if (!wait_pv(i_last)) return false;
-      const int slot = 2 * cid + slot1;
-      const float inv0 = t0 > 0.f ? 1.f / t0 : (t0 == 0.f ? 0.f : t0);
-      const float inv1 = t1 > 0.f ? 1.f / t1 : (t1 == 0.f ? 0.f : t1);
-      __nv_bfloat16* dst0 = (!partial ? p.omerged + ((size_t)bb * kH + row0) * kC
-                                      : p.opart + ((size_t)slot * kH + row0) * kC) +
-                            rank * 256 + 2 * c4;
-      __nv_bfloat16* dst1 = dst0 + 8 * kC;
-      uint32_t r[16];
-#pragma unroll 1
-      for (int cc = 0; cc < 256; cc += 32) {
-        tmem_ld_16x256b_x4(tmem + frag + T_O + cc, r);
-        tc_wait_ld();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          *reinterpret_cast<uint32_t*>(dst0 + cc + 8 * j) =
-              pack_bf16x2(u2f(r[4 * j]) * inv0, u2f(r[4 * j + 1]) * inv0);
-          *reinterpret_cast<uint32_t*>(dst1 + cc + 8 * j) =
-              pack_bf16x2(u2f(r[4 * j + 2]) * inv1, u2f(r[4 * j + 3]) * inv1);
-        }
-      }
-      tc_fence_before();
-      if (partial && rank == 0 && c4 == 0) {
-        float* lse = p.lse + (size_t)slot * kH;
-        lse[row0] = t0 == 0.f ? -INFINITY : m0 + log2f(t0);
-        lse[row1] = t1 == 0.f ? -INFINITY : m1 + log2f(t1);
-      }
-      return true;
-    };
-    float x[32];
-    Pos c = {bb0, jt0, tiles_of(bb0)};
-    int lim = lim_of(bb0);
-    int prev_bb = bb0, nx = 0;
-    bool open = false;  // the last tile processed is not its token's last
-    int nseg = 0;       // segments written out
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-      const int b = i & 1, ph = (i >> 1) & 1;
-      const bool first = i == 0 || c.jt == 0;
-      if (first && i > 0) {
-        if (!flush(i - 1, prev_bb, nseg == 0 && jt0 > 0, 0)) { alive = false; break; }
-        ++nseg;
-        m0 = m1 = -INFINITY;
-        l0 = l1 = 0.f;
-      }
-      if (!warp_wait(&bars.s_full[b], ph, abort, p.status)) { alive = false; break; }
-      tc_fence_after();
-      {
-        uint32_t own[32];
-        tmem_ld_16x256b_x8(tmem + frag + T_S + b * KT, own);
-        if (!warp_wait<true>(&bars.xs_full[b], ph, abort, p.status)) { alive = false; break; }
-        nx = i + 1;
-        uint4 v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = ld_shared_v4(xs_own + b * XS_BYTES + k * 512);
-        tc_wait_ld();
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          x[4 * k] = u2f(own[4 * k]) + u2f(v[k].x);
-          x[4 * k + 1] = u2f(own[4 * k + 1]) + u2f(v[k].y);
-          x[4 * k + 2] = u2f(own[4 * k + 2]) + u2f(v[k].z);
-          x[4 * k + 3] = u2f(own[4 * k + 3]) + u2f(v[k].w);
-        }
-      }
-      // the sums are computed (so the buffer's loads have returned) before the
-      // relaxed arrives below
-#pragma unroll
-      for (int j = 0; j < 32; ++j) asm volatile("" : "+f"(x[j]));
+    auto publish_m = [&](float m) {  // the running maximum after this group's tile
+      bars.m[g][h] = m;  // (both lanes of the head: the same value)
       __syncwarp();
-      if (lane == 0) {
-        if (warp == 0 && i + 2 < n) mbar_arrive_expect_tx_relaxed(&bars.xs_full[b], XS_BYTES);
-        mbar_arrive_cluster_relaxed(xs_free_peer + b * 8);
+      if (lane == 0) mbar_arrive(&bars.m_full[g][q4]);
+    };
+    float l = 0.f, lm = -INFINITY;  // this lane's and group's part of the row sum, its maximum
+    int bb = bb0, jt = jt0, nr = tiles_of(bb0), lim = lim_of(bb0);
+    int nseg = 0;  // tokens whose last tile came before this one
+    int lseg = 0;  // the segment that l belongs to
+    auto step = [&]() {
+      if (++jt == nr) {
+        jt = 0;
+        ++nseg;
+        nr = tiles_of(++bb);
+        lim = lim_of(bb);
       }
-      // scale to log2 units; mask the token's last tile; row maxima
-      const int left = lim - c.jt * KT;
-      float mt0 = -INFINITY, mt1 = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) x[j] *= p.scale_log2;
-      if (left < KT) {
+    };
+    if (g == 1) step();
+#pragma unroll 1
+    for (int i = g; i < n; i += 2) {
+      const int ph = (i >> 1) & 1;
+      const bool first = i == 0 || jt == 0;          // the segment's first tile
+      const bool ends = jt == nr - 1 || i == n - 1;  // ... its last
+      if (nseg != lseg) {  // this group's first tile of the segment
+        lseg = nseg;
+        l = 0.f;
+        lm = -INFINITY;
+      }
+      if (!warp_wait<true>(&bars.s_full[i % NSB], (i / NSB) & 1, abort, p.status)) break;
+      tc_fence_after();
+      float x[32];
+      tmem_ld32(tmem + lane_base + T_S + (i % NSB) * (KT / 2), reinterpret_cast<uint32_t*>(x));
+      tc_wait_ld();
+      const int left = lim - jt * KT - half * 32;
+      if (left < 32) {
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          if ((j >> 2) * 8 + 2 * c4 + (j & 1) >= left) x[j] = -INFINITY;
+          if (j >= left) x[j] = -INFINITY;
       }
+      float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        mt0 = fmaxf(mt0, fmaxf(x[4 * j], x[4 * j + 1]));
-        mt1 = fmaxf(mt1, fmaxf(x[4 * j + 2], x[4 * j + 3]));
-      }
+      for (int j = 4; j < 32; j += 4)
 #pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        mt0 = fmaxf(mt0, __shfl_xor_sync(0xffffffffu, mt0, o));
-        mt1 = fmaxf(mt1, __shfl_xor_sync(0xffffffffu, mt1, o));
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[j + e]);
+      // (log2 units; the scale is positive)
+      float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+      // The running maximum after tile i - 1, from the other group.  Waited for
+      // before this tile's maxima are exchanged: whoever passes the exchange
+      // then knows that both lanes' warps of the other group are done with
+      // tile i - 1, and a segment's last tile publishes only after it has
+      // read the sums of all four.
+      float m = -INFINITY;
+      if (i > 0) {
+        if (!warp_wait(&bars.m_full[g ^ 1][q4], ((i - 1) >> 1) & 1, abort, p.status)) break;
+        if (!first) m = *(volatile float*)&bars.m[g ^ 1][h];
       }
-      const bool resc0 = mt0 > m0 + kRescaleThreshold, resc1 = mt1 > m1 + kRescaleThreshold;
-      if (!first && __any_sync(0xffffffffu, resc0 || resc1)) {
+      // the tile's maximum over both lanes of the row
+      bars.x[g][ln] = mt;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.x_full[g][q4 & 1]);
+      if (!warp_wait(&bars.x_full[g][q4 & 1], ph, abort, p.status)) break;
+      mt = fmaxf(mt, *(volatile float*)&bars.x[g][ln ^ 64]);
+      const bool raise = mt > m + kRescaleThreshold;
+      const float mn = raise ? mt : m;
+      if (!ends) publish_m(mn);
+      if (!first && __any_sync(0xffffffffu, raise)) {
         // O~ must hold the value product of tile i - 1 before it is scaled
-        if (!wait_pv(i - 1)) { alive = false; break; }
-        rescale_o(resc0 ? fast_exp2(m0 - mt0) : 1.f, resc1 ? fast_exp2(m1 - mt1) : 1.f);
-      }
-      if (resc0) {
-        l0 *= first ? 0.f : fast_exp2(m0 - mt0);
-        m0 = mt0;
-      }
-      if (resc1) {
-        l1 *= first ? 0.f : fast_exp2(m1 - mt1);
-        m1 = mt1;
-      }
-      // P over the scores once the senders have read them too
-      {
-        // (a row that has seen no key yet has m = -inf: its P is exp2(-inf) = 0)
-        const float d0 = m0 == -INFINITY ? 0.f : m0, d1 = m1 == -INFINITY ? 0.f : m1;
-        uint32_t w[16];
-        float s0 = 0.f, s1 = 0.f;
+        if (!wait_pv(i - 1)) break;
+        const float a = raise ? fast_exp2(m - mn) : 1.f;
+#pragma unroll 1
+        for (int cc = 0; cc < 256; cc += 16) {
+          uint32_t r[16];
+          tmem_ld16(to + cc, r);
+          tc_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float e0 = fast_exp2(x[4 * j] - d0), e1 = fast_exp2(x[4 * j + 1] - d0);
-          const float e2 = fast_exp2(x[4 * j + 2] - d1), e3 = fast_exp2(x[4 * j + 3] - d1);
-          s0 += e0 + e1;
-          s1 += e2 + e3;
-          w[2 * j] = pack_bf16x2(e0, e1);
-          w[2 * j + 1] = pack_bf16x2(e2, e3);
+          for (int j = 0; j < 16; ++j) r[j] = f2u(u2f(r[j]) * a);
+          tmem_st16(to + cc, r);
         }
-        l0 += s0;
-        l1 += s1;
-        if (!warp_wait(&bars.sent[b], ph, abort, p.status)) { alive = false; break; }
-        tc_fence_after();
-        tmem_st_16x128b_x8(tmem + frag + T_S + b * KT, w);
+        tc_wait_st();
       }
-      tc_wait_st();
+      if (lm != mn) {  // the sum so far refers to a lower maximum (or is empty)
+        l *= lm == -INFINITY ? 0.f : fast_exp2(lm - mn);
+        lm = mn;
+      }
+      // (a row that has seen no key yet has m = -inf: its P is exp2(-inf) = 0)
+      const float d = mn == -INFINITY ? 0.f : -mn;
+      uint32_t w[16];
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float e0 = fast_exp2(fmaf(x[2 * j], p.scale_log2, d));
+        const float e1 = fast_exp2(fmaf(x[2 * j + 1], p.scale_log2, d));
+        s0 += e0;
+        s1 += e1;
+        w[j] = pack_bf16x2(e0, e1);
+      }
+      l += s0 + s1;
+      // the P buffer's last reader is the value product of tile i - 2
+      if (i >= 2 && !wait_pv(i - 2)) break;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        st_shared_v4(p_row + sw128_off(h, half * 4 + c), w[4 * c], w[4 * c + 1], w[4 * c + 2],
+                     w[4 * c + 3]);
+      // the previous token's output has left TMEM before this one's first
+      // value product (the other group writes it out)
+      if (first && i > 0 &&
+          !warp_wait(&bars.flushed[q4], (nseg - 1) & 1, abort, p.status))
+        break;
+      bars.l[g][ln] = l;
+      fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.p_full[b]);
-      prev_bb = c.bb;
-      open = c.jt != c.nr - 1;
-      if (++c.jt == c.nr) {
-        c.jt = 0;
-        c.nr = tiles_of(++c.bb);
-        lim = lim_of(c.bb);
+      if (lane == 0) {
+        mbar_arrive(&bars.l_full[g][q4]);
+        mbar_arrive_cluster(p_bar);
       }
+      if (ends) {
+        // the segment's end: the sums of both lanes and groups, then this lane's
+        // half of O~ / l into the token's output (a token held whole by this
+        // pair), or rounded to bf16 into the pair's slot (0: the range's first
+        // segment, 1: its last) with the segment's log-sum-exps
+        if (!warp_wait(&bars.l_full[g][q4 ^ 2], ph, abort, p.status)) break;
+        volatile float* sum = bars.l[g];
+        float lt = sum[h] + sum[h + 64];
+        if (!first) {
+          // tile i - 1 was the other group's, of the same segment: its sums refer
+          // to the maximum it published (and publishes again only after this one)
+          const int ph1 = ((i - 1) >> 1) & 1;
+          if (!warp_wait(&bars.l_full[g ^ 1][q4], ph1, abort, p.status) ||
+              !warp_wait(&bars.l_full[g ^ 1][q4 ^ 2], ph1, abort, p.status))
+            break;
+          sum = bars.l[g ^ 1];
+          const float l2 = sum[h] + sum[h + 64];
+          if (m != -INFINITY) lt += l2 * fast_exp2(m - mn);
+        }
+        publish_m(mn);
+        if (!wait_pv(i)) break;
+        const bool partial = (nseg == 0 && jt0 > 0) || jt != nr - 1;
+        const int slot = 2 * cid + (nseg == 0 ? 0 : 1);
+        const int head = rank * HH + h;
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;
+        __nv_bfloat16* dst = (!partial ? p.omerged + ((size_t)bb * kH + head) * kC
+                                       : p.opart + ((size_t)slot * kH + head) * kC) +
+                             half * 256;
+#pragma unroll 1
+        for (int cc = 0; cc < 256; cc += 32) {
+          uint32_t r[32];
+          tmem_ld32(to + cc, r);
+          tc_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(dst + cc + 8 * j) = make_uint4(
+                pack_bf16x2(u2f(r[8 * j]) * inv, u2f(r[8 * j + 1]) * inv),
+                pack_bf16x2(u2f(r[8 * j + 2]) * inv, u2f(r[8 * j + 3]) * inv),
+                pack_bf16x2(u2f(r[8 * j + 4]) * inv, u2f(r[8 * j + 5]) * inv),
+                pack_bf16x2(u2f(r[8 * j + 6]) * inv, u2f(r[8 * j + 7]) * inv));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.flushed[q4]);
+        if (partial && half == 0)
+          p.lse[(size_t)slot * kH + head] = lt == 0.f ? -INFINITY : mn + log2f(lt);
+      }
+      step();
+      step();
     }
-    // on an abort, partial scores the peer may still be sending land before
-    // the CTA can leave: the armed, unconsumed phases (none on the normal path)
-    for (int t = nx; t < n && t < nx + 2; ++t)
-      warp_wait<true>(&bars.xs_full[t & 1], (t >> 1) & 1, nullptr, nullptr);
-    if (__all_sync(0xffffffffu, alive) && !*abort)
-      flush(n - 1, prev_bb, (nseg == 0 && jt0 > 0) || open, nseg == 0 ? 0 : 1);
   }
 
   tc_fence_before();
   __syncthreads();
+  if (*abort) {
+    // a warp that gave up may leave loads in flight, which land within
+    // microseconds: a millisecond before the pair leaves
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000) {
+    }
+  }
+  cluster_sync_all();
   if (warp == MMA_WARP) {
     tc_fence_after();
-    tmem_dealloc(tmem, TMEM_COLS);
+    tmem_dealloc2(tmem, TMEM_COLS);
   }
-  // neither CTA leaves while its peer may still touch its shared memory
-  cluster_sync_all();
+  cluster_sync_all();  // neither CTA leaves before both have released
 }
 
 // ===========================================================================
@@ -1057,11 +998,11 @@ static int max_pairs() {
   attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(2 * kMaxPairs);
   cfg.blockDim = dim3(NTHREADS);
-  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.dynamicSmemBytes = dynamic_smem();
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaFuncSetAttribute(absorbed_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           SMEM_BYTES) != cudaSuccess ||
+                           dynamic_smem()) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&n, absorbed_kernel<false>, &cfg) != cudaSuccess || n < 1) {
     cudaGetLastError();
     int sms = 148;
@@ -1112,26 +1053,21 @@ static int launch_value_nb(const __nv_bfloat16* wkv_b, const __nv_bfloat16* omer
 
 template <bool kE4M3>
 static int launch_absorbed(const Params& p, int nc, cudaStream_t st) {
-  alignas(64) CUtensorMap map_c = {}, map_r = {}, map_c1 = {}, map_r1 = {};
+  alignas(64) CUtensorMap map_qt, map_qr, map_k = {}, map_v = {}, map_1 = {};
+  if (int e = bf16_map_3d(&map_qt, p.q_tilde, kC, kH, p.N, kC * 2, kH * kC * 2, 64, HH, 1))
+    return e;
+  if (int e = bf16_map_3d(&map_qr, p.q_pe, kR, kH, p.N, kR * 2, kH * kR * 2, 64, HH, 1)) return e;
   if (!kE4M3) {
-    const uint8_t* lat = p.pool.base;
-    const uint8_t* rot = p.pool.base + kC * 2;
     const uint64_t rows = p.pool.rows, rb = p.pool.row_stride;
-    const int box = p.box ? p.box : 1;
-    const auto l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
-    if (int e = bf16_map_2d(&map_c, lat, kC, rows, rb, 64, box, CU_TENSOR_MAP_SWIZZLE_128B, l2))
-      return e;
-    if (int e = bf16_map_2d(&map_r, rot, kR, rows, rb, 32, box, CU_TENSOR_MAP_SWIZZLE_64B, l2))
-      return e;
-    if (int e = bf16_map_2d(&map_c1, lat, kC, rows, rb, 64, 1, CU_TENSOR_MAP_SWIZZLE_128B, l2))
-      return e;
-    if (int e = bf16_map_2d(&map_r1, rot, kR, rows, rb, 32, 1, CU_TENSOR_MAP_SWIZZLE_64B, l2))
-      return e;
+    const int kbox = p.kbox ? p.kbox : 1, vbox = p.vbox ? p.vbox : 1;
+    if (int e = bf16_map_2d(&map_k, p.pool.base, MLA_ROW, rows, rb, 64, kbox)) return e;
+    if (int e = bf16_map_2d(&map_v, p.pool.base, MLA_ROW, rows, rb, 64, vbox)) return e;
+    if (int e = bf16_map_2d(&map_1, p.pool.base, MLA_ROW, rows, rb, 64, 1)) return e;
   }
   static std::atomic<unsigned long long> attr_done{0};
-  if (int e = ensure_smem_attr(absorbed_kernel<kE4M3>, SMEM_BYTES, &attr_done)) return e;
-  return launch_pdl(absorbed_kernel<kE4M3>, dim3(2 * nc), dim3(NTHREADS), SMEM_BYTES, st, p, map_c,
-                    map_r, map_c1, map_r1);
+  if (int e = ensure_smem_attr(absorbed_kernel<kE4M3>, dynamic_smem(), &attr_done)) return e;
+  return launch_pdl(absorbed_kernel<kE4M3>, dim3(2 * nc), dim3(NTHREADS), dynamic_smem(), st, p,
+                    map_qt, map_qr, map_k, map_v, map_1);
 }
 
 static int run_absorbed(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const mla_bf16_t* wkv_b,
@@ -1159,8 +1095,9 @@ static int run_absorbed(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const 
   p.pool = pool;
   p.plan = pl;
   p.N = q.N;
-  p.box = pool.page_size % 64 == 0 ? 64 : pool.page_size % 32 == 0 ? 32
-          : pool.page_size % 16 == 0 ? 16 : 0;
+  p.vbox = pool.page_size % 64 == 0 ? 64 : pool.page_size % 32 == 0 ? 32
+           : pool.page_size % 16 == 0 ? 16 : 0;
+  p.kbox = p.vbox < 32 ? p.vbox : 32;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.opart = reinterpret_cast<__nv_bfloat16*>(ws + L.opart);
   p.lse = reinterpret_cast<float*>(ws + L.lse);

@@ -456,7 +456,7 @@ int mla_page_read(const void* pool, int kind, int num_pages, int page_size, int6
  * tokens of the same call.  What the pages hold from kv_len[s] on does not
  * matter.
  * 1 <= N <= 65535, 1 <= S <= 65535, 1 <= max_kv <= 2^24; absorbed: N *
- * ceil(max_kv / 64) < 2^30; expanded: S * max_kv, each length rounded up to
+ * ceil(max_kv / 128) < 2^30; expanded: S * max_kv, each length rounded up to
  * 128, at most 2^26 (else MLA_ERR_SHAPE).  The expanded form's workspace holds
  * 1152 bytes for each of those positions and the keys and values of as many
  * heads as fit 4 GiB, at least 8 (4 KB a position) and at most 128 (64 KB).

@@ -5,7 +5,7 @@
 // Five kernels on the caller's stream:
 //
 //   plan_kernel      one block: each token's sequence and limit, the prefix sum
-//                    of the tokens' 64-key tiles, and its cut into one range
+//                    of the tokens' 128-key tiles, and its cut into one range
 //                    of equal cost per CTA pair
 //   (fold)           q~ per head, as in mla_decode
 //   absorbed_kernel  persistent CTA pairs over their ranges
@@ -25,9 +25,9 @@ namespace paged {
 // plan
 // ===========================================================================
 
-constexpr int KT = 64;  // keys per tile
+constexpr int KT = 128;  // keys per tile
 // Fixed cost of a token in tiles: its query load and its output's write-out.
-constexpr int kTokenCost = 4;
+constexpr int kTokenCost = 2;
 
 struct Plan {
   int32_t* seq;     // [N] sequence of each token
@@ -116,56 +116,66 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Seqs q, const Pool poo
 // TMEM.  So a pair shares a token: CTA r has heads [64r, +64), whose 64 rows of
 // scores and of output a pair's M = 128 product leaves in its own TMEM, each
 // row in two lanes: lane h the first half of the columns, lane 64 + h the
-// second.  No score ever crosses between the CTAs.  Per tile of 64 keys:
-//   S = Q~ K^T   M = 128, N = 64 keys, K = 576.  A: 64 rows of Q~ in each CTA.
-//                B: CTA r holds keys [32r, +32), all 576 columns.
-//   O += P V     M = 128, N = 2 x 256, K = 64 keys.  A: 64 rows of P in each
-//                CTA.  B: CTA r holds all 64 keys' latent columns [256r, +256),
+// second.  No score ever crosses between the CTAs.  Per tile of 128 keys:
+//   S = Q~ K^T   M = 128, N = 128 keys, K = 576.  A: 64 rows of Q~ in each CTA.
+//                B: CTA r holds keys [64r, +64), all 576 columns.
+//   O += P V     M = 128, N = 2 x 256, K = 128 keys.  A: 64 rows of P in each
+//                CTA.  B: CTA r holds all 128 keys' latent columns [256r, +256),
 //                read MN-major.
-// A row's two lanes hold 32 keys' scores each; they agree on the maximum
+// A row's two lanes hold 64 keys' scores each; they agree on the maximum
 // through shared memory.  fp32 online softmax: the running maximum is raised
 // only once a tile exceeds it by more than 8 log2 units; P = 2^(s-m) is rounded
 // to bf16 as a tensor-core operand (its row sum is of the fp32 P).
 //
-// Bounds, per tile and pair: 73.7 KB of cache (0.83 us at the measured copy
-// rate for 16-bit pages), 1456 cycles of products (36 x 26 + 8 x 65, measured;
-// 0.76 us at 1.92 GHz).  Keys and values are separate copies with rings of
-// their own (2 x 36 KB, 2 x 32 KB): a key slab is free once its scores are
-// computed, so its reload does not wait for the softmax.  (A pair that splits
-// the latent for scores too holds each value once, but must exchange 32 KB of
-// partial scores a tile; st.async moves them at 23 bytes a cycle and keeps the
-// other shared-memory accesses of the SM waiting: 3600 cycles a tile.)
+// Bounds, per tile and pair: 147 KB of cache (1.67 us at the measured copy rate
+// for 16-bit pages), 2196 cycles of products (measured alone, and not slower
+// with the loads running: 36 x 33 + 16 x 65; 1.14 us at 1.92 GHz).  Shared
+// memory holds one tile of keys and one of values, in three chunks of 192
+// columns and four of 32 keys, each reloaded as soon as its products are done:
+// the next tile's first chunk lands while this tile's last is in use, so the
+// reload waits neither for the softmax nor for the rest of the tile.
+// (Two rings of 64-key tiles took 2450 cycles a 64-key tile, waiting for the
+// reload of keys.  A pair that splits the latent for the scores too holds each
+// value once but must exchange 32 KB of partial scores per 64 keys; st.async
+// moves them at 23 bytes a cycle while the SM's other shared-memory accesses
+// wait: 3600 cycles.)
 //
 // Roles (640 threads a CTA):
 //   warps 0-7    softmax, two groups of four warps that take every other tile, a
 //                lane of TMEM per thread.  The running maximum goes from group
 //                to group (published as soon as a tile's is known, before its
 //                exponentials); row sums stay with the group until the token ends.
-//   warps 8-11   keys; 12-15 values.  16-bit pages: one warp of each, TMA boxes of
-//                up to 64 rows.  8-bit: loads, exact conversion to bf16 and
-//                swizzled stores.
+//   warps 8-11   keys; 12-15 values.  16-bit pages: one warp of each, TMA.  8-bit:
+//                loads, exact conversion to bf16 and swizzled stores.
 //   warp 16      MMA issuer (first CTA), TMEM owner
 //   warp 17      queries (TMA)
-// TMEM (512 columns): four score tiles [0,128), output [256,512).
+// TMEM (512 columns): four score tiles [0,256), output [256,512).
 // ===========================================================================
 
 constexpr int HH = kH / 2;             // heads of a CTA
-constexpr int NSB = 4;                 // score tiles in TMEM (32 columns each)
+constexpr int NSB = 4;                 // score tiles in TMEM (64 columns each)
+constexpr int NKC = 3, NVC = 4;        // chunks of a tile: 192 columns of keys, 32 keys of values
 constexpr int KEY_WARP0 = 8, VAL_WARP0 = 12, MMA_WARP = 16, Q_WARP = 17;
 constexpr int NTHREADS = 640;
 constexpr int Q_ATOM = HH * 128;       // 64 columns of 64 rows, 128 B swizzle
-constexpr int K_ATOM = KT / 2 * 128;   // 64 columns of 32 keys
-constexpr int V_ATOM = KT * 128;       // 64 columns of 64 keys
-constexpr int Q_BYTES = 9 * Q_ATOM, K_BYTES = 9 * K_ATOM, V_BYTES = 4 * V_ATOM;
+constexpr int K_ATOM = KT / 2 * 128;   // 64 columns of this CTA's 64 keys
+constexpr int V_ATOM = 32 * 128;       // 64 columns of a chunk's 32 keys
+constexpr int Q_BYTES = 9 * Q_ATOM, K_BYTES = 9 * K_ATOM, V_CHUNK = 4 * V_ATOM;
 constexpr int P_BYTES = HH * 128;      // 64 rows of 64 weights
 constexpr int OFF_K = Q_BYTES;
-constexpr int OFF_V = OFF_K + 2 * K_BYTES;
-constexpr int OFF_P = OFF_V + 2 * V_BYTES;
+constexpr int OFF_V = OFF_K + K_BYTES;
+constexpr int OFF_P = OFF_V + NVC * V_CHUNK;
 constexpr int SMEM_BYTES = OFF_P + 2 * P_BYTES;
 constexpr uint32_t T_S = 0, T_O = 256, TMEM_COLS = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 static_assert(OFF_K % 1024 == 0 && OFF_V % 1024 == 0 && OFF_P % 1024 == 0, "alignment");
 static_assert(T_S + NSB * KT / 2 <= T_O, "TMEM plan");
+// registers: 96 a thread at launch, five groups of four warps
+template <bool kE4M3>
+struct Regs {
+  static constexpr int soft = kE4M3 ? 120 : 128, load = kE4M3 ? 88 : 80, rest = 64;
+  static_assert(2 * soft + 2 * load + rest <= 5 * 96, "register split");
+};
 
 struct Params {
   const __nv_bfloat16* q_tilde;  // [N][128][512]
@@ -173,7 +183,7 @@ struct Params {
   Pool pool;
   Plan plan;
   int N;
-  int kbox, vbox;                // rows of a TMA box of keys (16, 32; 0: row by row) and values
+  int box;                       // rows of a TMA box that no page boundary cuts (64, 32; 0: none)
   float scale_log2;              // softmax scale * log2(e)
   __nv_bfloat16* opart;          // [pairs][2 slots][128][512], normalised per segment
   float* lse;                    // [pairs][2 slots][128], log2 units of scaled scores
@@ -183,13 +193,15 @@ struct Params {
 
 // "first CTA": waited on by the issuer only, arrived on from both CTAs;
 // "both": committed to both CTAs by the issuer; the others are each CTA's own
-struct Bars {
+struct alignas(16) Bars {
   uint64_t q_full, q_free;           // first CTA / both
-  uint64_t k_full[2], k_empty[2];    // first CTA / both
-  uint64_t v_full[2], v_empty[2];
+  uint64_t k_full[NKC], k_empty[NKC];  // first CTA / both
+  uint64_t v_full[NVC], v_empty[NVC];
   uint64_t s_full[NSB];              // both: scores of tile i in buffer i % NSB
-  uint64_t p_full[2];                // first CTA: P of tile i in buffer i & 1
-  uint64_t o_done[2];                // both: value product of tile i done
+  uint64_t p_full[2][2];             // first CTA, by group: [0] first half of P written and all of O
+                                     // free to be added to, [1] second half written
+  uint64_t p_empty[2][2];            // both: P of tile i used, by i & 1 and half of the keys
+  uint64_t o_done[2];                // both: value product of tile i (i & 1) done
   uint64_t m_full[2][4];             // running maxima after tile i, by group and lane quarter
   uint64_t x_full[2][2];             // tile maxima of both lanes of a row (by quarter & 1)
   uint64_t l_full[2][4];             // row sums after tile i
@@ -256,12 +268,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     constexpr int fill = kE4M3 ? 8 : 1;  // four warps of each CTA, or one arrival and bytes
     mbar_init(&bars.q_full, 1);
     mbar_init(&bars.q_free, 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NKC; ++i) {
       mbar_init(&bars.k_full[i], fill);
-      mbar_init(&bars.v_full[i], fill);
       mbar_init(&bars.k_empty[i], 1);
+    }
+    for (int i = 0; i < NVC; ++i) {
+      mbar_init(&bars.v_full[i], fill);
       mbar_init(&bars.v_empty[i], 1);
-      mbar_init(&bars.p_full[i], 8);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.p_full[i][0], 8);  // the four warps of a group in each CTA
+      mbar_init(&bars.p_full[i][1], 4);  // the two of the second half
+      mbar_init(&bars.p_empty[i][0], 1);
+      mbar_init(&bars.p_empty[i][1], 1);
       mbar_init(&bars.o_done[i], 1);
       mbar_init(&bars.x_full[i][0], 2);
       mbar_init(&bars.x_full[i][1], 2);
@@ -285,187 +304,201 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     // an empty range (fewer tiles than pairs): nothing to do
   } else if (warp >= KEY_WARP0 && warp < MMA_WARP) {
     // ---------------- keys and values ----------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kE4M3>::load));
     const bool val = warp >= VAL_WARP0;
     const int w4 = warp & 3;
-    uint64_t* full = val ? bars.v_full : bars.k_full;
-    uint64_t* empty = val ? bars.v_empty : bars.k_empty;
-    const uint32_t full0 = first_cta(full);
-    if (kE4M3 || w4 == 0) {
-      // this CTA's rows of a tile: 32 keys, or all 64 for values.  Lane l holds
-      // the pool rows of the l-th and (values) the (32 + l)-th.
-      const int sub = val ? 0 : rank * 32;
-      int bb = bb0, jt = jt0 - 1, nr = tiles_of(bb0), lim = 0, bad = 0;
-      const int32_t* trow = nullptr;
-      bool last = false;  // the token sees all its sequence's positions: count its bad pages
-      auto enter = [&]() {
-        if (bb >= p.N) return;
-        const int s = ld_global_nc_s32_early(p.plan.seq + bb);
-        lim = lim_of(bb);
-        trow = p.pool.table + (long long)s * p.pool.max_pages;
-        last = bb + 1 >= ld_global_nc_s32_early(p.plan.nact) ||
-               ld_global_nc_s32_early(p.plan.seq + bb + 1) != s;
-      };
-      enter();
-      int ra = 0, rb = 0, key0 = 0;
-      auto next_tile = [&]() {
-        if (++jt == nr) {
-          jt = 0;
-          nr = tiles_of(++bb);
-          enter();
-        }
-        key0 = jt * KT + sub;
-        ra = rb = p.pool.rows;
-        if (key0 + lane < lim) ra = row_of(p.pool, trow, key0 + lane);
-        if (val && key0 + 32 + lane < lim) rb = row_of(p.pool, trow, key0 + 32 + lane);
+    // Groups of 32 keys: two a tile for keys (this CTA's 64), four for values.
+    // Lane l looks up the page of each group's l-th key, a tile ahead: r[g] is
+    // its pool row for the current tile, pg[g] its page for the next.
+    const int groups = val ? NVC : 2, sub = val ? 0 : rank * 64;
+    int bb = bb0, jt = jt0 - 1, nr = tiles_of(bb0), nlim = 0, lim = 0, key0 = 0, bad = 0;
+    const int32_t* trow = nullptr;
+    bool last = false;  // the token sees all its sequence's positions: count its bad pages
+    int r[NVC], pg[NVC];
+    auto enter = [&]() {
+      if (bb >= p.N) return;
+      const int s = ld_global_nc_s32_early(p.plan.seq + bb);
+      nlim = lim_of(bb);
+      trow = p.pool.table + (long long)s * p.pool.max_pages;
+      last = bb + 1 >= ld_global_nc_s32_early(p.plan.nact) ||
+             ld_global_nc_s32_early(p.plan.seq + bb + 1) != s;
+    };
+    auto fetch = [&]() {  // the next tile's pages
+      if (++jt == nr) {
+        jt = 0;
+        nr = tiles_of(++bb);
+        enter();
+      }
+#pragma unroll
+      for (int g = 0; g < NVC; ++g) {
+        const int k = jt * KT + sub + g * 32 + lane;
+        pg[g] = g < groups && k < nlim ? ld_global_nc_s32_early(trow + k / p.pool.page_size) : -1;
+      }
+    };
+    auto enter_tile = [&](bool more) {  // the fetched tile becomes the current one
+      lim = nlim;
+      key0 = jt * KT + sub;
+#pragma unroll
+      for (int g = 0; g < NVC; ++g) {
+        const int k = key0 + g * 32 + lane, o = k % p.pool.page_size;
+        const bool in = pg[g] >= 0 && pg[g] < p.pool.num_pages;
+        r[g] = in ? pg[g] * p.pool.pitch + o : p.pool.rows;
         // entries outside the pool, each page of a sequence once
-        if (val && rank == 0 && w4 == 0 && last) {
-          const int a = key0 + lane, b = a + 32;
-          bad += a < lim && ra == p.pool.rows && a % p.pool.page_size == 0;
-          bad += b < lim && rb == p.pool.rows && b % p.pool.page_size == 0;
-        }
-      };
-      // the pool row of the tile's row k (whole warp)
-      auto row = [&](int k) {
-        const int ya = __shfl_sync(0xffffffffu, ra, k & 31);
-        const int yb = __shfl_sync(0xffffffffu, rb, k & 31);
-        return k < 32 ? ya : yb;
-      };
-      next_tile();
-      if constexpr (!kE4M3) {
-        const int rows = val ? KT : KT / 2, box = val ? p.vbox : p.kbox;
-        const int atoms = val ? 4 : 9, x0 = val ? rank * 256 : 0;
-        const int bytes = val ? V_BYTES : K_BYTES, atom_bytes = rows * 128;
-        const CUtensorMap* map = val ? &map_v : &map_k;
+        if (val && rank == 0 && w4 == 0 && last) bad += !in && k < lim && o == 0;
+      }
+      if (more) fetch();
+    };
+    enter();
+    fetch();
+    if constexpr (!kE4M3) {
+      if (w4 == 0) {
+        const uint32_t full0 = first_cta(val ? &bars.v_full[0] : &bars.k_full[0]);
+        uint64_t* full = val ? bars.v_full : bars.k_full;
+        uint64_t* empty = val ? bars.v_empty : bars.k_empty;
+        const int chunks = val ? NVC : NKC, bytes = val ? V_CHUNK : 3 * K_ATOM;
+        const uint32_t base = sbase + (val ? OFF_V : OFF_K);
+        bool ok = true;
 #pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-          const int s = i & 1;
-          const bool boxes = box && key0 + rows <= lim;
-          int y[4];
-          int k0;
-          if (boxes) {
-            // whole boxes of rows: every page boundary is a box boundary
-            k0 = (lane * box) & (rows - 1);
-            y[0] = row(k0);
-          } else {
-            // row by row: the tile's rows past the limit read as zeros, so
-            // that nothing stored there can reach a product
-            k0 = (4 * lane) & (rows - 1);
+        for (int i = 0; i < n && ok; ++i) {
+          enter_tile(i + 1 < n);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] = row(k0 + j);
-          }
-          if (i + 1 < n) next_tile();
-          if (!warp_wait(&empty[s], ((i >> 1) & 1) ^ 1, abort, p.status)) break;
-          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
-          __syncwarp();
-          const uint32_t slab = sbase + (val ? OFF_V : OFF_K) + s * bytes;
-          const uint32_t bar = full0 + s * 8;
-          if (boxes) {
-            if (lane * box < rows)
-              for (int a = 0; a < atoms; ++a)
-                tma_load_2d_pair(slab + a * atom_bytes + k0 * 128, map, x0 + a * 64, y[0], bar);
-          } else if (lane * 4 < rows) {
-            for (int a = 0; a < atoms; ++a)
-              tma_gather4_pair(slab + a * atom_bytes + k0 * 128, &map_1, x0 + a * 64, y[0], y[1],
-                               y[2], y[3], bar);
-          }
-        }
-      } else if (!val) {
-        // 8-bit keys: a row per step and warp, 16 codes per lane
-        uint4 code[8], rope[2];
-        float sc[8];
-        auto load = [&]() {
+          for (int c = 0; c < NVC; ++c) {
+            if (c >= chunks || !ok) continue;
+            ok = warp_wait(&empty[c], (i & 1) ^ 1, abort, p.status);
+            if (!ok) continue;
+            if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&full[c], 2 * bytes);
+            __syncwarp();
+            const uint32_t bar = full0 + c * 8, dst = base + c * bytes;
+            // The box's rows lie in one page and below the limit: one load.
+            // Otherwise row by row, four rows a load: rows past the limit read
+            // as zeros, so that nothing stored there can reach a product.
+            if (val) {
+              const int y0 = __shfl_sync(0xffffffffu, r[c], 0);
+              if (p.box >= 32 && key0 + c * 32 + 32 <= lim) {
+                if (lane == 0) tma_load_3d_pair(dst, &map_v, 0, y0, rank * 4, bar);
+              } else {
+                const int g = lane & 7, a = lane >> 3;  // rows 4g .. 4g+3, column atom
+                int y[4];
 #pragma unroll
-          for (int it = 0; it < 8; ++it) {
-            const int y = row(w4 * 8 + it);
-            code[it] = make_uint4(0, 0, 0, 0);
-            sc[it] = 1.f;
-            if (y < p.pool.rows) {
-              const uint8_t* src = p.pool.base + (long long)y * p.pool.row_stride;
-              code[it] = ld_global_nc_v4(src + lane * 16);
-              sc[it] = u2f((uint32_t)ld_global_nc_s32_early(
-                  reinterpret_cast<const int32_t*>(src + pages::kScaleOff + (lane >> 3) * 4)));
+                for (int j = 0; j < 4; ++j) y[j] = __shfl_sync(0xffffffffu, r[c], 4 * g + j);
+                tma_gather4_pair(dst + a * V_ATOM + g * 512, &map_1, rank * 256 + a * 64, y[0],
+                                 y[1], y[2], y[3], bar);
+              }
+            } else {
+              const int y0 = __shfl_sync(0xffffffffu, r[0], 0);
+              if (p.box == 64 && key0 + 64 <= lim) {
+                if (lane == 0) tma_load_3d_pair(dst, &map_k, 0, y0, c * 3, bar);
+              } else {
+                const int g = lane & 15;  // rows 4g .. 4g+3
+                int y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int ya = __shfl_sync(0xffffffffu, r[0], (4 * g + j) & 31);
+                  const int yb = __shfl_sync(0xffffffffu, r[1], (4 * g + j) & 31);
+                  y[j] = g < 8 ? ya : yb;
+                }
+                for (int a = lane >> 4; a < 3; a += 2)
+                  tma_gather4_pair(dst + a * K_ATOM + g * 512, &map_1, (c * 3 + a) * 64, y[0],
+                                   y[1], y[2], y[3], bar);
+              }
             }
           }
-#pragma unroll
-          for (int it = 0; it < 2; ++it) {
-            const int y = row(w4 * 8 + it * 4 + (lane >> 3));
-            rope[it] = make_uint4(0, 0, 0, 0);
-            if (y < p.pool.rows)
-              rope[it] = ld_global_nc_v4(p.pool.base + (long long)y * p.pool.row_stride +
-                                         pages::kRopeOff + (lane & 7) * 16);
-          }
-        };
-        load();
-#pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-          const int s = i & 1;
-          if (i + 1 < n) next_tile();
-          if (!warp_wait(&empty[s], ((i >> 1) & 1) ^ 1, abort, p.status)) break;
-          const uint32_t slab = sbase + OFF_K + s * K_BYTES;
-#pragma unroll
-          for (int it = 0; it < 8; ++it) {
-            const int r = w4 * 8 + it, c = (lane & 3) * 2;
-            const uint32_t atom = slab + (lane >> 2) * K_ATOM;
-            uint4 o0, o1;
-            pages::dequant16(code[it], sc[it], o0, o1);
-            st_shared_v4(atom + sw128_off(r, c), o0.x, o0.y, o0.z, o0.w);
-            st_shared_v4(atom + sw128_off(r, c + 1), o1.x, o1.y, o1.z, o1.w);
-          }
-#pragma unroll
-          for (int it = 0; it < 2; ++it)
-            st_shared_v4(slab + 8 * K_ATOM + sw128_off(w4 * 8 + it * 4 + (lane >> 3), lane & 7),
-                         rope[it].x, rope[it].y, rope[it].z, rope[it].w);
-          if (i + 1 < n) load();
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(full0 + s * 8);
-        }
-      } else {
-        // 8-bit values: two rows per step and warp, 16 codes per lane
-        const int rsel = lane >> 4, ch = lane & 15;
-        uint4 code[8];
-        float sc[8];
-        auto load = [&]() {
-#pragma unroll
-          for (int it = 0; it < 8; ++it) {
-            const int y = row(w4 * 16 + it * 2 + rsel);
-            code[it] = make_uint4(0, 0, 0, 0);
-            sc[it] = 1.f;
-            if (y < p.pool.rows) {
-              const uint8_t* src = p.pool.base + (long long)y * p.pool.row_stride;
-              code[it] = ld_global_nc_v4(src + rank * 256 + ch * 16);
-              sc[it] = u2f((uint32_t)ld_global_nc_s32_early(reinterpret_cast<const int32_t*>(
-                  src + pages::kScaleOff + (rank * 2 + (ch >> 3)) * 4)));
-            }
-          }
-        };
-        load();
-#pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-          const int s = i & 1;
-          if (i + 1 < n) next_tile();
-          if (!warp_wait(&empty[s], ((i >> 1) & 1) ^ 1, abort, p.status)) break;
-          const uint32_t slab = sbase + OFF_V + s * V_BYTES;
-#pragma unroll
-          for (int it = 0; it < 8; ++it) {
-            const int r = w4 * 16 + it * 2 + rsel, c = (ch & 3) * 2;
-            const uint32_t atom = slab + (ch >> 2) * V_ATOM;
-            uint4 o0, o1;
-            pages::dequant16(code[it], sc[it], o0, o1);
-            st_shared_v4(atom + sw128_off(r, c), o0.x, o0.y, o0.z, o0.w);
-            st_shared_v4(atom + sw128_off(r, c + 1), o1.x, o1.y, o1.z, o1.w);
-          }
-          if (i + 1 < n) load();
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(full0 + s * 8);
         }
       }
-      bad = __reduce_add_sync(0xffffffffu, bad);
-      if (lane == 0 && bad && p.status) atomicAdd(p.status + 1, bad);
+    } else {
+      // 8-bit: steps of 512 units of 16 codes, four a thread of the four warps,
+      // the next step's loads issued before this one's conversion.  Keys: 16
+      // rows of 32 units a step (and one 16-byte piece of a rotary key a
+      // thread); values: 32 rows (a chunk) of 16 units.
+      uint4 code[4], rope, ncode[4], nrope;
+      float sc[4], nsc[4];
+      const int ch = val ? lane & 15 : lane;
+      const int ugrp = val ? rank * 2 + (ch >> 3) : lane >> 3;   // its scale
+      const int uoff = val ? rank * 256 + ch * 16 : lane * 16;   // its codes
+      // row within the 32-key group of unit `it` of step half `st`
+      auto unit_row = [&](int st, int it) {
+        return val ? w4 * 8 + it * 2 + (lane >> 4) : st * 16 + w4 * 4 + it;
+      };
+      auto load = [&](int st, int rows) {  // rows: the group's pool rows
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          const int y = __shfl_sync(0xffffffffu, rows, unit_row(st, it));
+          ncode[it] = make_uint4(0, 0, 0, 0);
+          nsc[it] = 1.f;
+          if (y < p.pool.rows) {
+            const uint8_t* src = p.pool.base + (long long)y * p.pool.row_stride;
+            ncode[it] = ld_global_nc_v4(src + uoff);
+            nsc[it] = u2f((uint32_t)ld_global_nc_s32_early(
+                reinterpret_cast<const int32_t*>(src + pages::kScaleOff + ugrp * 4)));
+          }
+        }
+        if (!val) {
+          const int y = __shfl_sync(0xffffffffu, rows, st * 16 + w4 * 4 + (lane >> 3));
+          nrope = make_uint4(0, 0, 0, 0);
+          if (y < p.pool.rows)
+            nrope = ld_global_nc_v4(p.pool.base + (long long)y * p.pool.row_stride +
+                                    pages::kRopeOff + (lane & 7) * 16);
+        }
+      };
+      const uint32_t full0 = first_cta(val ? &bars.v_full[0] : &bars.k_full[0]);
+      bool ok = true;
+      enter_tile(n > 1);
+      load(0, r[0]);
+#pragma unroll 1
+      for (int i = 0; i < n && ok; ++i) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+            code[it] = ncode[it];
+            sc[it] = nsc[it];
+          }
+          rope = nrope;
+          if (c < 3) {
+            load((c + 1) & 1, val ? r[c + 1] : r[(c + 1) >> 1]);
+          } else if (i + 1 < n) {
+            enter_tile(i + 2 < n);
+            load(0, r[0]);
+          }
+          // (keys: the last chunk's products are the last to finish)
+          if (ok && (val || c == 0))
+            ok = warp_wait(val ? &bars.v_empty[c] : &bars.k_empty[NKC - 1], (i & 1) ^ 1, abort,
+                           p.status);
+          if (!ok) continue;
+          const uint32_t atom = val ? sbase + OFF_V + c * V_CHUNK + (ch >> 2) * V_ATOM
+                                    : sbase + OFF_K + (lane >> 2) * K_ATOM;
+          const int c2 = (ch & 3) * 2;
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+            const int row = unit_row(c & 1, it) + (val ? 0 : (c >> 1) * 32);
+            uint4 o0, o1;
+            pages::dequant16(code[it], sc[it], o0, o1);
+            st_shared_v4(atom + sw128_off(row, c2), o0.x, o0.y, o0.z, o0.w);
+            st_shared_v4(atom + sw128_off(row, c2 + 1), o1.x, o1.y, o1.z, o1.w);
+          }
+          if (!val)
+            st_shared_v4(sbase + OFF_K + 8 * K_ATOM +
+                             sw128_off(c * 16 + w4 * 4 + (lane >> 3), lane & 7),
+                         rope.x, rope.y, rope.z, rope.w);
+          if (val || c == 3) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (val) {
+                mbar_arrive_cluster(full0 + c * 8);
+              } else {
+                for (int k = 0; k < NKC; ++k) mbar_arrive_cluster(full0 + k * 8);
+              }
+            }
+          }
+        }
+      }
     }
+    bad = __reduce_add_sync(0xffffffffu, bad);
+    if (lane == 0 && bad && p.status) atomicAdd(p.status + 1, bad);
   } else if (warp == Q_WARP) {
     // ---------------- queries: this CTA's 64 heads of each token ----------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kE4M3>::rest));
     pdl_wait();  // q~ is the fold kernel's output (the other roles read only inputs and the plan)
     const uint32_t bar = first_cta(&bars.q_full);
     int bb = bb0, i = 0;
@@ -482,70 +515,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     }
   } else if (warp == MMA_WARP) {
     // ---------------- MMA issuer ----------------
-    // A value product goes first whenever its P is ready, then the score
-    // product of a tile whose keys have landed and whose buffer's earlier
-    // scores both CTAs have turned into a P.
+    // Chunk by chunk: a value chunk whose P and values are there goes first,
+    // then a score chunk whose keys have landed (and, for a tile's first one,
+    // whose buffer's earlier scores both CTAs have turned into a P).
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kE4M3>::rest));
     if (rank == 0) {
       constexpr uint32_t idesc_qk = idesc_bf16_f32(128, KT, 0, 0);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(128, 256, 0, 1);
       constexpr uint32_t hi128 = desc_hi(1024, kSwizzle128B);
-      const uint32_t lo_q = desc_lo(sbase, 16);
+      const uint32_t lo_q = desc_lo(sbase, 16), lo_k = desc_lo(sbase + OFF_K, 16);
+      const uint32_t lo_v = desc_lo(sbase + OFF_V, V_ATOM), lo_p = desc_lo(sbase + OFF_P, 16);
       auto test = [](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_test_cluster(bar, parity)) != 0;
       };
       Pos cq = {bb0, jt0, tiles_of(bb0)}, cv = cq;  // tiles of the next score / value product
-      int qk = 0, pv = 0, idle = 0, seg = 0;
+      int qk = 0, qc = 0, pv = 0, vc = 0;           // tile and chunk of each
+      int idle = 0, seg = 0;
       uint64_t t_idle = 0;
 #pragma unroll 1
       while (pv < n) {
         bool did = false;
-        if (pv < qk && test(&bars.p_full[pv & 1], (pv >> 1) & 1) &&
-            test(&bars.v_full[pv & 1], (pv >> 1) & 1)) {
+        if ((pv < qk) && ((vc & 1) || test(&bars.p_full[pv & 1][vc >> 1], (pv >> 1) & 1)) &&
+            test(&bars.v_full[vc], pv & 1)) {
           tc_fence_after();
-          const uint32_t lo_v = desc_lo(sbase + OFF_V + (pv & 1) * V_BYTES, V_ATOM);  // MN-major
-          const uint32_t lo_p = desc_lo(sbase + OFF_P + (pv & 1) * P_BYTES, 16);
-          const uint32_t first = pv == 0 || cv.jt == 0 ? 1u : 0u;
+          const uint32_t first = vc == 0 && (pv == 0 || cv.jt == 0) ? 1u : 0u;
+          const uint32_t a = lo_p + ((vc >> 1) * P_BYTES + (vc & 1) * 64) / 16;
+          const uint32_t v = lo_v + vc * (V_CHUNK / 16);
           if (elect_one()) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-              for (int ks = 0; ks < KT / 16; ++ks)
-                tc_mma2(tmem + T_O + j * 128, desc_join(lo_p + ks * 2, hi128),
-                        desc_join(lo_v + ((j * 2 * V_ATOM + ks * 2048) >> 4), hi128), idesc_pv,
+              for (int j = 0; j < 2; ++j)
+                tc_mma2(tmem + T_O + j * 128, desc_join(a + ks * 2, hi128),
+                        desc_join(v + (j * 2 * V_ATOM + ks * 2048) / 16, hi128), idesc_pv,
                         ks > 0 ? 1u : first ^ 1u);
-            tc_commit2(&bars.o_done[pv & 1]);
-            tc_commit2(&bars.v_empty[pv & 1]);
+            tc_commit2(&bars.v_empty[vc]);
+            if (vc & 1) tc_commit2(&bars.p_empty[pv & 1][vc >> 1]);
+            if (vc == NVC - 1) tc_commit2(&bars.o_done[pv & 1]);
           }
           __syncwarp();
-          ++pv;
-          if (++cv.jt == cv.nr) {
-            cv.jt = 0;
-            cv.nr = tiles_of(++cv.bb);
+          if (++vc == NVC) {
+            vc = 0;
+            ++pv;
+            if (++cv.jt == cv.nr) {
+              cv.jt = 0;
+              cv.nr = tiles_of(++cv.bb);
+            }
           }
           did = true;
         }
-        if (qk < n && qk < pv + NSB && test(&bars.k_full[qk & 1], (qk >> 1) & 1) &&
-            test(&bars.q_full, seg & 1)) {
+        if (qk < n && qk < pv + NSB && test(&bars.k_full[qc], qk & 1) &&
+            (qc > 0 || test(&bars.q_full, seg & 1))) {
           tc_fence_after();
-          const uint32_t lo_k = desc_lo(sbase + OFF_K + (qk & 1) * K_BYTES, 16);
           const uint32_t ts = tmem + T_S + (qk % NSB) * (KT / 2);
-          const bool ends = cq.jt == cq.nr - 1;
+          const uint32_t a = lo_q + qc * (3 * Q_ATOM / 16), k = lo_k + qc * (3 * K_ATOM / 16);
+          const bool ends = qc == NKC - 1 && cq.jt == cq.nr - 1;
           if (elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < 36; ++ks)
-              tc_mma2(ts, desc_join(lo_q + (((ks >> 2) * Q_ATOM + (ks & 3) * 32) >> 4), hi128),
-                      desc_join(lo_k + (((ks >> 2) * K_ATOM + (ks & 3) * 32) >> 4), hi128),
-                      idesc_qk, ks > 0 ? 1u : 0u);
-            tc_commit2(&bars.s_full[qk % NSB]);
-            tc_commit2(&bars.k_empty[qk & 1]);
+            for (int ks = 0; ks < 12; ++ks)
+              tc_mma2(ts, desc_join(a + ((ks >> 2) * Q_ATOM + (ks & 3) * 32) / 16, hi128),
+                      desc_join(k + ((ks >> 2) * K_ATOM + (ks & 3) * 32) / 16, hi128), idesc_qk,
+                      ks > 0 || qc > 0 ? 1u : 0u);
+            tc_commit2(&bars.k_empty[qc]);
+            if (qc == NKC - 1) tc_commit2(&bars.s_full[qk % NSB]);
             if (ends) tc_commit2(&bars.q_free);
           }
           __syncwarp();
-          ++qk;
-          if (++cq.jt == cq.nr) {
-            cq.jt = 0;
-            cq.nr = tiles_of(++cq.bb);
-            ++seg;
+          if (++qc == NKC) {
+            qc = 0;
+            ++qk;
+            if (++cq.jt == cq.nr) {
+              cq.jt = 0;
+              cq.nr = tiles_of(++cq.bb);
+              ++seg;
+            }
           }
           did = true;
         }
@@ -572,7 +615,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       __syncwarp();
       warp_wait<true>(&bars.drain, 0, nullptr, p.status);
     }
-  } else if (warp < KEY_WARP0) {
+  } else if (warp >= KEY_WARP0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kE4M3>::rest));  // (idle)
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<kE4M3>::soft));
     // ---------------- softmax: group g = tiles i with i % 2 == g ----------------
     // Thread = TMEM lane: head h = lane % 64 of this CTA's, keys (and latent
     // columns) of half lane / 64.
@@ -580,8 +626,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     const int ln = q4 * 32 + lane, h = ln & 63, half = ln >> 6;
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
     const uint32_t to = tmem + lane_base + T_O;
-    const uint32_t p_row = sbase + OFF_P + g * P_BYTES;
-    const uint32_t p_bar = first_cta(&bars.p_full[g]);
+    const uint32_t p_row = sbase + OFF_P + half * P_BYTES;
+    const uint32_t p_bar0 = first_cta(&bars.p_full[g][0]), p_bar = p_bar0 + half * 8;
     auto wait_pv = [&](int t) -> bool {  // the value product of tile t has completed
       if (!warp_wait<true>(&bars.o_done[t & 1], (t >> 1) & 1, abort, p.status)) return false;
       tc_fence_after();
@@ -617,18 +663,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       }
       if (!warp_wait<true>(&bars.s_full[i % NSB], (i / NSB) & 1, abort, p.status)) break;
       tc_fence_after();
-      float x[32];
-      tmem_ld32(tmem + lane_base + T_S + (i % NSB) * (KT / 2), reinterpret_cast<uint32_t*>(x));
+      float x[64];
+      const uint32_t ts = tmem + lane_base + T_S + (i % NSB) * (KT / 2);
+      tmem_ld32(ts, reinterpret_cast<uint32_t*>(x));
+      tmem_ld32(ts + 32, reinterpret_cast<uint32_t*>(x) + 32);
       tc_wait_ld();
-      const int left = lim - jt * KT - half * 32;
-      if (left < 32) {
+      const int left = lim - jt * KT - half * 64;
+      if (left < 64) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < 64; ++j)
           if (j >= left) x[j] = -INFINITY;
       }
       float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int j = 4; j < 32; j += 4)
+      for (int j = 4; j < 64; j += 4)
 #pragma unroll
         for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[j + e]);
       // (log2 units; the scale is positive)
@@ -673,10 +721,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       }
       // (a row that has seen no key yet has m = -inf: its P is exp2(-inf) = 0)
       const float d = mn == -INFINITY ? 0.f : -mn;
-      uint32_t w[16];
+      uint32_t w[32];
       float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
+      for (int j = 0; j < 32; ++j) {
         const float e0 = fast_exp2(fmaf(x[2 * j], p.scale_log2, d));
         const float e1 = fast_exp2(fmaf(x[2 * j + 1], p.scale_log2, d));
         s0 += e0;
@@ -684,25 +732,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         w[j] = pack_bf16x2(e0, e1);
       }
       l += s0 + s1;
-      // the P buffer's last reader is the value product of tile i - 2
-      if (i >= 2 && !wait_pv(i - 2)) break;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        st_shared_v4(p_row + sw128_off(h, half * 4 + c), w[4 * c], w[4 * c + 1], w[4 * c + 2],
-                     w[4 * c + 3]);
       // the previous token's output has left TMEM before this one's first
       // value product (the other group writes it out)
       if (first && i > 0 &&
           !warp_wait(&bars.flushed[q4], (nseg - 1) & 1, abort, p.status))
         break;
       bars.l[g][ln] = l;
-      fence_proxy_async_smem();
+      // (an arrival below is for this tile's phase: the group's last one, of
+      // tile i - 2, is over once its value product has used the first half)
+      if (i >= 2 && !warp_wait<true>(&bars.p_empty[g][0], ((i - 2) >> 1) & 1, abort, p.status))
+        break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&bars.l_full[g][q4]);
-        mbar_arrive_cluster(p_bar);
+        // The first half's products write all lanes of O: these warps' lanes
+        // are ready, so those products need not wait for the second half of P.
+        if (half == 1) mbar_arrive_cluster(p_bar0);
       }
+      // This half of P has been used by tile i - 1's value product.  (A barrier
+      // for each parity of tiles: a group waits on every phase of its own, and
+      // one that both waited on could be two phases behind what a wait expects.)
+      if (i > 0 && !warp_wait<true>(&bars.p_empty[g ^ 1][half], ((i - 1) >> 1) & 1, abort, p.status))
+        break;
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        st_shared_v4(p_row + sw128_off(h, c), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(p_bar);
       if (ends) {
         // the segment's end: the sums of both lanes and groups, then this lane's
         // half of O~ / l into the token's output (a token held whole by this
@@ -1058,10 +1116,10 @@ static int launch_absorbed(const Params& p, int nc, cudaStream_t st) {
     return e;
   if (int e = bf16_map_3d(&map_qr, p.q_pe, kR, kH, p.N, kR * 2, kH * kR * 2, 64, HH, 1)) return e;
   if (!kE4M3) {
+    // rows as [9 column atoms][rows][64]: a box takes several atoms at once
     const uint64_t rows = p.pool.rows, rb = p.pool.row_stride;
-    const int kbox = p.kbox ? p.kbox : 1, vbox = p.vbox ? p.vbox : 1;
-    if (int e = bf16_map_2d(&map_k, p.pool.base, MLA_ROW, rows, rb, 64, kbox)) return e;
-    if (int e = bf16_map_2d(&map_v, p.pool.base, MLA_ROW, rows, rb, 64, vbox)) return e;
+    if (int e = bf16_map_3d(&map_k, p.pool.base, 64, rows, 9, rb, 128, 64, 64, 3)) return e;
+    if (int e = bf16_map_3d(&map_v, p.pool.base, 64, rows, 9, rb, 128, 64, 32, 4)) return e;
     if (int e = bf16_map_2d(&map_1, p.pool.base, MLA_ROW, rows, rb, 64, 1)) return e;
   }
   static std::atomic<unsigned long long> attr_done{0};
@@ -1095,9 +1153,7 @@ static int run_absorbed(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const 
   p.pool = pool;
   p.plan = pl;
   p.N = q.N;
-  p.vbox = pool.page_size % 64 == 0 ? 64 : pool.page_size % 32 == 0 ? 32
-           : pool.page_size % 16 == 0 ? 16 : 0;
-  p.kbox = p.vbox < 32 ? p.vbox : 32;
+  p.box = pool.page_size % 64 == 0 ? 64 : pool.page_size % 32 == 0 ? 32 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.opart = reinterpret_cast<__nv_bfloat16*>(ws + L.opart);
   p.lse = reinterpret_cast<float*>(ws + L.lse);
@@ -1132,9 +1188,9 @@ static int check_sizes(int N, int S, int max_kv, int form) {
   if (N < 1 || N > 65535 || S < 1 || S > 65535 || max_kv < 1 || max_kv > (1 << 24))
     return MLA_ERR_SHAPE;
   if (form < MLA_FORM_AUTO || form > MLA_FORM_EXPANDED) return MLA_ERR_SHAPE;
-  // absorbed: the flattened list of (token, 64-key tile) is counted in 32 bits
+  // absorbed: the flattened list of (token, 128-key tile) is counted in 32 bits
   if (form_of(form, N, S) == MLA_FORM_EXPANDED ? !expand::fits(S, max_kv)
-                                               : (int64_t)N * ((max_kv + 63) / 64) > 0x3fffffff)
+                                               : (int64_t)N * ((max_kv + 127) / 128) > 0x3fffffff)
     return MLA_ERR_SHAPE;
   return MLA_OK;
 }

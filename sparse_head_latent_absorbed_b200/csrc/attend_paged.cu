@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Seqs q, const Pool poo
 // for 16-bit pages), 2196 cycles of products (measured alone, and not slower
 // with the loads running: 36 x 33 + 16 x 65; 1.14 us at 1.92 GHz).  Shared
 // memory holds one tile of keys and one of values, in three chunks of 192
-// columns and four of 32 keys, each reloaded as soon as its products are done:
+// columns and two of 64 keys, each reloaded as soon as its products are done:
 // the next tile's first chunk lands while this tile's last is in use, so the
 // reload waits neither for the softmax nor for the rest of the tile.
 // (Two rings of 64-key tiles took 2450 cycles a 64-key tile, waiting for the
@@ -145,26 +145,29 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Seqs q, const Pool poo
 //                lane of TMEM per thread.  The running maximum goes from group
 //                to group (published as soon as a tile's is known, before its
 //                exponentials); row sums stay with the group until the token ends.
-//   warps 8-11   keys; 12-15 values.  16-bit pages: one warp of each, TMA.  8-bit:
+//   warps 8-11   keys; 12-15 values.  16-bit pages: a warp for each chunk, TMA (one
+//                warp for all chunks took 700 cycles for each, in turn).  8-bit:
 //                loads, exact conversion to bf16 and swizzled stores.
-//   warp 16      MMA issuer (first CTA), TMEM owner
+//   warp 16      issues the score products (first CTA), TMEM owner
 //   warp 17      queries (TMA)
+//   warp 18      issues the value products (first CTA).  One warp for both spent
+//                4400 cycles a tile in barrier tests and issues.
 // TMEM (512 columns): four score tiles [0,256), output [256,512).
 // ===========================================================================
 
 constexpr int HH = kH / 2;             // heads of a CTA
 constexpr int NSB = 4;                 // score tiles in TMEM (64 columns each)
-constexpr int NKC = 3, NVC = 4;        // chunks of a tile: 192 columns of keys, 32 keys of values
-constexpr int KEY_WARP0 = 8, VAL_WARP0 = 12, MMA_WARP = 16, Q_WARP = 17;
+constexpr int NKC = 3;                 // chunks of a tile's keys (192 columns); values: two of 64 keys
+constexpr int KEY_WARP0 = 8, VAL_WARP0 = 12, S_WARP = 16, Q_WARP = 17, O_WARP = 18;
 constexpr int NTHREADS = 640;
 constexpr int Q_ATOM = HH * 128;       // 64 columns of 64 rows, 128 B swizzle
 constexpr int K_ATOM = KT / 2 * 128;   // 64 columns of this CTA's 64 keys
-constexpr int V_ATOM = 32 * 128;       // 64 columns of a chunk's 32 keys
+constexpr int V_ATOM = 64 * 128;       // 64 columns of a chunk's 64 keys
 constexpr int Q_BYTES = 9 * Q_ATOM, K_BYTES = 9 * K_ATOM, V_CHUNK = 4 * V_ATOM;
 constexpr int P_BYTES = HH * 128;      // 64 rows of 64 weights
 constexpr int OFF_K = Q_BYTES;
 constexpr int OFF_V = OFF_K + K_BYTES;
-constexpr int OFF_P = OFF_V + NVC * V_CHUNK;
+constexpr int OFF_P = OFF_V + 2 * V_CHUNK;
 constexpr int SMEM_BYTES = OFF_P + 2 * P_BYTES;
 constexpr uint32_t T_S = 0, T_O = 256, TMEM_COLS = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
@@ -183,7 +186,7 @@ struct Params {
   Pool pool;
   Plan plan;
   int N;
-  int box;                       // rows of a TMA box that no page boundary cuts (64, 32; 0: none)
+  int box;                       // rows of a TMA box that no page boundary cuts (64, 32, 16; 0: none)
   float scale_log2;              // softmax scale * log2(e)
   __nv_bfloat16* opart;          // [pairs][2 slots][128][512], normalised per segment
   float* lse;                    // [pairs][2 slots][128], log2 units of scaled scores
@@ -196,17 +199,18 @@ struct Params {
 struct alignas(16) Bars {
   uint64_t q_full, q_free;           // first CTA / both
   uint64_t k_full[NKC], k_empty[NKC];  // first CTA / both
-  uint64_t v_full[NVC], v_empty[NVC];
+  uint64_t v_full[2];                // by half of the keys (two chunks)
   uint64_t s_full[NSB];              // both: scores of tile i in buffer i % NSB
+  uint64_t s_empty[NSB];             // first CTA: ... read by all softmax warps
   uint64_t p_full[2][2];             // first CTA, by group: [0] first half of P written and all of O
                                      // free to be added to, [1] second half written
-  uint64_t p_empty[2][2];            // both: P of tile i used, by i & 1 and half of the keys
-  uint64_t o_done[2];                // both: value product of tile i (i & 1) done
+  uint64_t pv_done[2][2];            // both: tile i's value products of a half of the keys done, by
+                                     // i & 1 and half: their P and values are free; [.][1]: O~ holds tile i
   uint64_t m_full[2][4];             // running maxima after tile i, by group and lane quarter
   uint64_t x_full[2][2];             // tile maxima of both lanes of a row (by quarter & 1)
   uint64_t l_full[2][4];             // row sums after tile i
   uint64_t flushed[4];               // a token's output has left TMEM, by lane quarter
-  uint64_t drain;                    // both
+  uint64_t drain[2];                 // both
   uint32_t tmem_base;
   int abort;
   // by group: running maxima of the heads, tile maxima and row sums of the lanes
@@ -232,6 +236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     const __grid_constant__ CUtensorMap map_qr,
                     const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v,
+                    const __grid_constant__ CUtensorMap map_b,
                     const __grid_constant__ CUtensorMap map_1) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -263,7 +268,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   // a barrier of the pair's first CTA
   auto first_cta = [&](uint64_t* bar) { return mapa_shared(smem_u32(bar), 0); };
 
-  if (warp == MMA_WARP) tmem_alloc2(&bars.tmem_base, TMEM_COLS);
+  if (warp == S_WARP) tmem_alloc2(&bars.tmem_base, TMEM_COLS);
   if (tid == 0) {
     constexpr int fill = kE4M3 ? 8 : 1;  // four warps of each CTA, or one arrival and bytes
     mbar_init(&bars.q_full, 1);
@@ -272,16 +277,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       mbar_init(&bars.k_full[i], fill);
       mbar_init(&bars.k_empty[i], 1);
     }
-    for (int i = 0; i < NVC; ++i) {
-      mbar_init(&bars.v_full[i], fill);
-      mbar_init(&bars.v_empty[i], 1);
-    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.p_full[i][0], 8);  // the four warps of a group in each CTA
       mbar_init(&bars.p_full[i][1], 4);  // the two of the second half
-      mbar_init(&bars.p_empty[i][0], 1);
-      mbar_init(&bars.p_empty[i][1], 1);
-      mbar_init(&bars.o_done[i], 1);
+      mbar_init(&bars.v_full[i], fill);
+      mbar_init(&bars.pv_done[i][0], 1);
+      mbar_init(&bars.pv_done[i][1], 1);
       mbar_init(&bars.x_full[i][0], 2);
       mbar_init(&bars.x_full[i][1], 2);
       for (int q = 0; q < 4; ++q) {
@@ -289,9 +290,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         mbar_init(&bars.l_full[i][q], 1);
       }
     }
-    for (int i = 0; i < NSB; ++i) mbar_init(&bars.s_full[i], 1);
+    for (int i = 0; i < NSB; ++i) {
+      mbar_init(&bars.s_full[i], 1);
+      mbar_init(&bars.s_empty[i], 8);
+    }
     for (int q = 0; q < 4; ++q) mbar_init(&bars.flushed[q], 1);
-    mbar_init(&bars.drain, 1);
+    mbar_init(&bars.drain[0], 1);
+    mbar_init(&bars.drain[1], 1);
     bars.abort = 0;
     fence_mbarrier_init_cluster();
   }
@@ -302,107 +307,102 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 
   if (n <= 0) {
     // an empty range (fewer tiles than pairs): nothing to do
-  } else if (warp >= KEY_WARP0 && warp < MMA_WARP) {
+  } else if (warp >= KEY_WARP0 && warp < S_WARP) {
     // ---------------- keys and values ----------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kE4M3>::load));
     const bool val = warp >= VAL_WARP0;
     const int w4 = warp & 3;
-    // Groups of 32 keys: two a tile for keys (this CTA's 64), four for values.
-    // Lane l looks up the page of each group's l-th key, a tile ahead: r[g] is
-    // its pool row for the current tile, pg[g] its page for the next.
-    const int groups = val ? NVC : 2, sub = val ? 0 : rank * 64;
-    int bb = bb0, jt = jt0 - 1, nr = tiles_of(bb0), nlim = 0, lim = 0, key0 = 0, bad = 0;
+    int bb = bb0, jt = jt0 - 1, nr = tiles_of(bb0), lim = 0, bad = 0;
     const int32_t* trow = nullptr;
     bool last = false;  // the token sees all its sequence's positions: count its bad pages
-    int r[NVC], pg[NVC];
     auto enter = [&]() {
       if (bb >= p.N) return;
       const int s = ld_global_nc_s32_early(p.plan.seq + bb);
-      nlim = lim_of(bb);
+      lim = lim_of(bb);
       trow = p.pool.table + (long long)s * p.pool.max_pages;
       last = bb + 1 >= ld_global_nc_s32_early(p.plan.nact) ||
              ld_global_nc_s32_early(p.plan.seq + bb + 1) != s;
     };
-    auto fetch = [&]() {  // the next tile's pages
+    auto advance = [&]() {  // to the next tile
       if (++jt == nr) {
         jt = 0;
         nr = tiles_of(++bb);
         enter();
       }
-#pragma unroll
-      for (int g = 0; g < NVC; ++g) {
-        const int k = jt * KT + sub + g * 32 + lane;
-        pg[g] = g < groups && k < nlim ? ld_global_nc_s32_early(trow + k / p.pool.page_size) : -1;
-      }
     };
-    auto enter_tile = [&](bool more) {  // the fetched tile becomes the current one
-      lim = nlim;
-      key0 = jt * KT + sub;
-#pragma unroll
-      for (int g = 0; g < NVC; ++g) {
-        const int k = key0 + g * 32 + lane, o = k % p.pool.page_size;
-        const bool in = pg[g] >= 0 && pg[g] < p.pool.num_pages;
-        r[g] = in ? pg[g] * p.pool.pitch + o : p.pool.rows;
-        // entries outside the pool, each page of a sequence once
-        if (val && rank == 0 && w4 == 0 && last) bad += !in && k < lim && o == 0;
-      }
-      if (more) fetch();
+    // an entry outside the pool counts once for each page of a sequence
+    auto row_at = [&](int pg, int off, bool count) {
+      const bool in = pg >= 0 && pg < p.pool.num_pages;
+      if (count && !in && off == 0) ++bad;
+      return in ? pg * p.pool.pitch + off : p.pool.rows;
     };
     enter();
-    fetch();
     if constexpr (!kE4M3) {
-      if (w4 == 0) {
-        const uint32_t full0 = first_cta(val ? &bars.v_full[0] : &bars.k_full[0]);
-        uint64_t* full = val ? bars.v_full : bars.k_full;
-        uint64_t* empty = val ? bars.v_empty : bars.k_empty;
-        const int chunks = val ? NVC : NKC, bytes = val ? V_CHUNK : 3 * K_ATOM;
-        const uint32_t base = sbase + (val ? OFF_V : OFF_K);
-        bool ok = true;
+      const int chunk = w4;  // of the keys' columns, or of the values' keys
+      if (chunk < (val ? 2 : NKC)) {
+        const int sub = val ? chunk * 64 : rank * 64;  // this chunk's first key in a tile
+        uint64_t* const full = val ? &bars.v_full[chunk] : &bars.k_full[chunk];
+        const uint32_t bar = first_cta(full);
+        const uint32_t dst = sbase + (val ? OFF_V + chunk * V_CHUNK : OFF_K + chunk * 3 * K_ATOM);
+        const int bytes = val ? V_CHUNK : 3 * K_ATOM, atoms = val ? 4 : 3;
+        const int atom0 = val ? rank * 4 : chunk * 3;  // 64-column atom of the row
+        const CUtensorMap* const map = val ? &map_v : &map_k;
+        const bool counts = val && rank == 0;  // the values' warps of one CTA see every key once
+        // The page of a box of 64 keys is looked up a tile ahead.
+        int pg = -1;
+        auto lookup = [&]() {
+          advance();
+          const int k = jt * KT + sub;
+          if (p.box == 64 && k + 64 <= lim) pg = ld_global_nc_s32_early(trow + k / p.pool.page_size);
+        };
+        lookup();
 #pragma unroll 1
-        for (int i = 0; i < n && ok; ++i) {
-          enter_tile(i + 1 < n);
-#pragma unroll
-          for (int c = 0; c < NVC; ++c) {
-            if (c >= chunks || !ok) continue;
-            ok = warp_wait(&empty[c], (i & 1) ^ 1, abort, p.status);
-            if (!ok) continue;
-            if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&full[c], 2 * bytes);
-            __syncwarp();
-            const uint32_t bar = full0 + c * 8, dst = base + c * bytes;
-            // The box's rows lie in one page and below the limit: one load.
-            // Otherwise row by row, four rows a load: rows past the limit read
-            // as zeros, so that nothing stored there can reach a product.
-            if (val) {
-              const int y0 = __shfl_sync(0xffffffffu, r[c], 0);
-              if (p.box >= 32 && key0 + c * 32 + 32 <= lim) {
-                if (lane == 0) tma_load_3d_pair(dst, &map_v, 0, y0, rank * 4, bar);
-              } else {
-                const int g = lane & 7, a = lane >> 3;  // rows 4g .. 4g+3, column atom
-                int y[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = __shfl_sync(0xffffffffu, r[c], 4 * g + j);
-                tma_gather4_pair(dst + a * V_ATOM + g * 512, &map_1, rank * 256 + a * 64, y[0],
-                                 y[1], y[2], y[3], bar);
-              }
-            } else {
-              const int y0 = __shfl_sync(0xffffffffu, r[0], 0);
-              if (p.box == 64 && key0 + 64 <= lim) {
-                if (lane == 0) tma_load_3d_pair(dst, &map_k, 0, y0, c * 3, bar);
-              } else {
-                const int g = lane & 15;  // rows 4g .. 4g+3
-                int y[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const int ya = __shfl_sync(0xffffffffu, r[0], (4 * g + j) & 31);
-                  const int yb = __shfl_sync(0xffffffffu, r[1], (4 * g + j) & 31);
-                  y[j] = g < 8 ? ya : yb;
-                }
-                for (int a = lane >> 4; a < 3; a += 2)
-                  tma_gather4_pair(dst + a * K_ATOM + g * 512, &map_1, (c * 3 + a) * 64, y[0],
-                                   y[1], y[2], y[3], bar);
-              }
-            }
+        for (int i = 0; i < n; ++i) {
+          const int k0 = jt * KT + sub, left = lim - k0;
+          const bool whole = p.box == 64 && left >= 64;
+          int y0 = 0, r0 = p.pool.rows, r1 = p.pool.rows;  // rows of keys k0, k0 + lane, k0 + 32 + lane
+          if (whole) {
+            y0 = row_at(pg, k0 % p.pool.page_size, counts && last && lane == 0);
+          } else {
+            const int ka = k0 + lane, kb = ka + 32, ps = p.pool.page_size;
+            if (ka < lim) r0 = row_at(ld_global_nc_s32_early(trow + ka / ps), ka % ps, counts && last);
+            if (kb < lim) r1 = row_at(ld_global_nc_s32_early(trow + kb / ps), kb % ps, counts && last);
           }
+          if (i + 1 < n) lookup();
+          const bool ok =
+              val ? i == 0 || warp_wait(&bars.pv_done[(i - 1) & 1][chunk], ((i - 1) >> 1) & 1,
+                                        abort, p.status)
+                  : warp_wait(&bars.k_empty[chunk], (i & 1) ^ 1, abort, p.status);
+          if (!ok) break;
+          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(full, 2 * bytes);
+          __syncwarp();
+          if (whole) {
+            if (elect_one()) tma_load_3d_pair(dst, map, 0, y0, atom0, bar);
+          } else if (p.box && left >= 64) {
+            // pages of a multiple of 16 or 32 rows: a box for each column atom
+            const int per = 64 / p.box, k = (lane % per) * p.box, a = lane / per;
+            const int ya = __shfl_sync(0xffffffffu, r0, k & 31);
+            const int yb = __shfl_sync(0xffffffffu, r1, k & 31);
+            if (a < atoms)
+              tma_load_2d_pair(dst + a * 8192 + k * 128, &map_b, (atom0 + a) * 64,
+                               k < 32 ? ya : yb, bar);
+          } else {
+            // row by row, four rows a load: the rows past the limit read as
+            // zeros, so that nothing stored there can reach a product
+            const int g = lane & 15;  // rows 4g .. 4g+3
+            int y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int ya = __shfl_sync(0xffffffffu, r0, (4 * g + j) & 31);
+              const int yb = __shfl_sync(0xffffffffu, r1, (4 * g + j) & 31);
+              y[j] = g < 8 ? ya : yb;
+            }
+#pragma unroll 1
+            for (int a = lane >> 4; a < atoms; a += 2)
+              tma_gather4_pair(dst + a * 8192 + g * 512, &map_1, (atom0 + a) * 64, y[0], y[1],
+                               y[2], y[3], bar);
+          }
+          __syncwarp();
         }
       }
     } else {
@@ -410,6 +410,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       // the next step's loads issued before this one's conversion.  Keys: 16
       // rows of 32 units a step (and one 16-byte piece of a rotary key a
       // thread); values: 32 rows (a chunk) of 16 units.
+      // Groups of 32 keys: two a tile for keys (this CTA's 64), four for values.
+      // Lane l looks up the page of each group's l-th key, a tile ahead: r[g] is
+      // its pool row for the current tile, pg[g] its page for the next.
+      const int groups = val ? 4 : 2, sub = val ? 0 : rank * 64;
+      int r[4], pg[4];
+      auto fetch = [&]() {  // the next tile's pages
+        advance();
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int k = jt * KT + sub + g * 32 + lane;
+          pg[g] = -2;
+          if (g < groups && k < lim) pg[g] = ld_global_nc_s32_early(trow + k / p.pool.page_size);
+        }
+      };
+      auto enter_tile = [&](bool more) {  // the fetched tile becomes the current one
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int k = jt * KT + sub + g * 32 + lane;
+          r[g] = row_at(pg[g], k % p.pool.page_size,
+                        val && rank == 0 && w4 == 0 && last && k < lim);
+        }
+        if (more) fetch();
+      };
+      fetch();
       uint4 code[4], rope, ncode[4], nrope;
       float sc[4], nsc[4];
       const int ch = val ? lane & 15 : lane;
@@ -446,7 +470,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       load(0, r[0]);
 #pragma unroll 1
       for (int i = 0; i < n && ok; ++i) {
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
 #pragma unroll
           for (int it = 0; it < 4; ++it) {
@@ -455,22 +479,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           }
           rope = nrope;
           if (c < 3) {
-            load((c + 1) & 1, val ? r[c + 1] : r[(c + 1) >> 1]);
+            const int g = val ? c + 1 : (c + 1) >> 1;
+            load((c + 1) & 1, g == 0 ? r[0] : g == 1 ? r[1] : g == 2 ? r[2] : r[3]);
           } else if (i + 1 < n) {
             enter_tile(i + 2 < n);
             load(0, r[0]);
           }
           // (keys: the last chunk's products are the last to finish)
-          if (ok && (val || c == 0))
-            ok = warp_wait(val ? &bars.v_empty[c] : &bars.k_empty[NKC - 1], (i & 1) ^ 1, abort,
+          if (!val) {
+            if (c == 0) ok = warp_wait(&bars.k_empty[NKC - 1], (i & 1) ^ 1, abort, p.status);
+          } else if (i > 0 && (c & 1) == 0 && ok) {
+            ok = warp_wait(&bars.pv_done[(i - 1) & 1][c >> 1], ((i - 1) >> 1) & 1, abort,
                            p.status);
-          if (!ok) continue;
-          const uint32_t atom = val ? sbase + OFF_V + c * V_CHUNK + (ch >> 2) * V_ATOM
+          }
+          if (!ok) break;
+          const uint32_t atom = val ? sbase + OFF_V + (c >> 1) * V_CHUNK + (ch >> 2) * V_ATOM
                                     : sbase + OFF_K + (lane >> 2) * K_ATOM;
           const int c2 = (ch & 3) * 2;
 #pragma unroll
           for (int it = 0; it < 4; ++it) {
-            const int row = unit_row(c & 1, it) + (val ? 0 : (c >> 1) * 32);
+            const int row = unit_row(c & 1, it) + (val ? c & 1 : c >> 1) * 32;
             uint4 o0, o1;
             pages::dequant16(code[it], sc[it], o0, o1);
             st_shared_v4(atom + sw128_off(row, c2), o0.x, o0.y, o0.z, o0.w);
@@ -480,14 +508,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             st_shared_v4(sbase + OFF_K + 8 * K_ATOM +
                              sw128_off(c * 16 + w4 * 4 + (lane >> 3), lane & 7),
                          rope.x, rope.y, rope.z, rope.w);
-          if (val || c == 3) {
+          if (val ? (c & 1) : c == 3) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
               if (val) {
-                mbar_arrive_cluster(full0 + c * 8);
+                mbar_arrive_pair(full0 + (c >> 1) * 8);
               } else {
-                for (int k = 0; k < NKC; ++k) mbar_arrive_cluster(full0 + k * 8);
+                for (int k = 0; k < NKC; ++k) mbar_arrive_pair(full0 + k * 8);
               }
             }
           }
@@ -513,107 +541,94 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       __syncwarp();
       i += tiles_of(bb) - (seg == 0 ? jt0 : 0);
     }
-  } else if (warp == MMA_WARP) {
-    // ---------------- MMA issuer ----------------
-    // Chunk by chunk: a value chunk whose P and values are there goes first,
-    // then a score chunk whose keys have landed (and, for a tile's first one,
-    // whose buffer's earlier scores both CTAs have turned into a P).
+  } else if (warp == S_WARP) {
+    // ---------------- score products ----------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kE4M3>::rest));
     if (rank == 0) {
-      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, KT, 0, 0);
-      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, 256, 0, 1);
+      constexpr uint32_t idesc = idesc_bf16_f32(128, KT, 0, 0);
       constexpr uint32_t hi128 = desc_hi(1024, kSwizzle128B);
       const uint32_t lo_q = desc_lo(sbase, 16), lo_k = desc_lo(sbase + OFF_K, 16);
-      const uint32_t lo_v = desc_lo(sbase + OFF_V, V_ATOM), lo_p = desc_lo(sbase + OFF_P, 16);
-      auto test = [](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_test_cluster(bar, parity)) != 0;
-      };
-      Pos cq = {bb0, jt0, tiles_of(bb0)}, cv = cq;  // tiles of the next score / value product
-      int qk = 0, qc = 0, pv = 0, vc = 0;           // tile and chunk of each
-      int idle = 0, seg = 0;
-      uint64_t t_idle = 0;
+      int bb = bb0, jt = jt0, nr = tiles_of(bb0), seg = 0;
+      bool ok = true, fresh = true;  // fresh: the segment's queries have not been waited for
 #pragma unroll 1
-      while (pv < n) {
-        bool did = false;
-        if ((pv < qk) && ((vc & 1) || test(&bars.p_full[pv & 1][vc >> 1], (pv >> 1) & 1)) &&
-            test(&bars.v_full[vc], pv & 1)) {
+      for (int i = 0; i < n && ok; ++i) {
+        if (fresh) ok = warp_wait(&bars.q_full, seg & 1, abort, p.status);
+        fresh = false;
+        const int sb = i % NSB;
+        const bool ends = jt == nr - 1;
+        ok = ok && warp_wait(&bars.s_empty[sb], ((i / NSB) & 1) ^ 1, abort, p.status);
+        const uint32_t ts = tmem + T_S + sb * (KT / 2);
+#pragma unroll 1
+        for (int a = 0; a < 9 && ok; ++a) {  // 64-column atoms, three a chunk
+          const int c = a / 3;
+          if (a == 3 * c) ok = warp_wait(&bars.k_full[c], i & 1, abort, p.status);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t first = vc == 0 && (pv == 0 || cv.jt == 0) ? 1u : 0u;
-          const uint32_t a = lo_p + ((vc >> 1) * P_BYTES + (vc & 1) * 64) / 16;
-          const uint32_t v = lo_v + vc * (V_CHUNK / 16);
           if (elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                tc_mma2(tmem + T_O + j * 128, desc_join(a + ks * 2, hi128),
-                        desc_join(v + (j * 2 * V_ATOM + ks * 2048) / 16, hi128), idesc_pv,
-                        ks > 0 ? 1u : first ^ 1u);
-            tc_commit2(&bars.v_empty[vc]);
-            if (vc & 1) tc_commit2(&bars.p_empty[pv & 1][vc >> 1]);
-            if (vc == NVC - 1) tc_commit2(&bars.o_done[pv & 1]);
+            for (int ks = 0; ks < 4; ++ks)
+              tc_mma2(ts, desc_join(lo_q + (a * Q_ATOM + ks * 32) / 16, hi128),
+                      desc_join(lo_k + (a * K_ATOM + ks * 32) / 16, hi128), idesc,
+                      ks > 0 || a > 0 ? 1u : 0u);
+            if (a == 3 * c + 2) tc_commit2(&bars.k_empty[c]);
+            if (a == 8) {
+              tc_commit2(&bars.s_full[sb]);
+              if (ends) tc_commit2(&bars.q_free);
+            }
           }
           __syncwarp();
-          if (++vc == NVC) {
-            vc = 0;
-            ++pv;
-            if (++cv.jt == cv.nr) {
-              cv.jt = 0;
-              cv.nr = tiles_of(++cv.bb);
-            }
-          }
-          did = true;
         }
-        if (qk < n && qk < pv + NSB && test(&bars.k_full[qc], qk & 1) &&
-            (qc > 0 || test(&bars.q_full, seg & 1))) {
-          tc_fence_after();
-          const uint32_t ts = tmem + T_S + (qk % NSB) * (KT / 2);
-          const uint32_t a = lo_q + qc * (3 * Q_ATOM / 16), k = lo_k + qc * (3 * K_ATOM / 16);
-          const bool ends = qc == NKC - 1 && cq.jt == cq.nr - 1;
-          if (elect_one()) {
-#pragma unroll
-            for (int ks = 0; ks < 12; ++ks)
-              tc_mma2(ts, desc_join(a + ((ks >> 2) * Q_ATOM + (ks & 3) * 32) / 16, hi128),
-                      desc_join(k + ((ks >> 2) * K_ATOM + (ks & 3) * 32) / 16, hi128), idesc_qk,
-                      ks > 0 || qc > 0 ? 1u : 0u);
-            tc_commit2(&bars.k_empty[qc]);
-            if (qc == NKC - 1) tc_commit2(&bars.s_full[qk % NSB]);
-            if (ends) tc_commit2(&bars.q_free);
-          }
-          __syncwarp();
-          if (++qc == NKC) {
-            qc = 0;
-            ++qk;
-            if (++cq.jt == cq.nr) {
-              cq.jt = 0;
-              cq.nr = tiles_of(++cq.bb);
-              ++seg;
-            }
-          }
-          did = true;
-        }
-        if (did) {
-          idle = 0;
-          t_idle = 0;
-        } else if (++idle >= 64) {
-          idle = 0;
-          if (__any_sync(0xffffffffu, *abort != 0)) break;
-          const uint64_t now = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
-          if (t_idle == 0) {
-            t_idle = now;
-          } else if (now - t_idle > kWaitLimitNs) {
-            if (lane == 0) {
-              *abort = 1;
-              report_timeout(p.status);
-            }
-            break;
-          }
+        if (++jt == nr) {
+          jt = 0;
+          nr = tiles_of(++bb);
+          ++seg;
+          fresh = true;
         }
       }
       // everything issued so far has finished before TMEM is released
-      if (elect_one()) tc_commit2(&bars.drain);
+      if (elect_one()) tc_commit2(&bars.drain[0]);
       __syncwarp();
-      warp_wait<true>(&bars.drain, 0, nullptr, p.status);
+      warp_wait(&bars.drain[0], 0, nullptr, p.status);
+    }
+  } else if (warp == O_WARP) {
+    // ---------------- value products ----------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kE4M3>::rest));
+    if (rank == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128, 256, 0, 1);
+      constexpr uint32_t hi128 = desc_hi(1024, kSwizzle128B);
+      const uint32_t lo_v = desc_lo(sbase + OFF_V, V_ATOM), lo_p = desc_lo(sbase + OFF_P, 16);
+      int bb = bb0, jt = jt0, nr = tiles_of(bb0);
+      bool ok = true;
+#pragma unroll 1
+      for (int i = 0; i < n && ok; ++i) {
+        const uint32_t first = i == 0 || jt == 0 ? 1u : 0u;
+#pragma unroll 1
+        for (int c = 0; c < 2 && ok; ++c) {  // half of the keys
+          ok = warp_wait(&bars.v_full[c], i & 1, abort, p.status) &&
+               warp_wait(&bars.p_full[i & 1][c], (i >> 1) & 1, abort, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = lo_p + c * (P_BYTES / 16), v = lo_v + c * (V_CHUNK / 16);
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                tc_mma2(tmem + T_O + j * 128, desc_join(a + ks * 2, hi128),
+                        desc_join(v + (j * 2 * V_ATOM + ks * 2048) / 16, hi128), idesc,
+                        ks > 0 || c > 0 ? 1u : first ^ 1u);
+            tc_commit2(&bars.pv_done[i & 1][c]);
+          }
+          __syncwarp();
+        }
+        if (++jt == nr) {
+          jt = 0;
+          nr = tiles_of(++bb);
+        }
+      }
+      if (elect_one()) tc_commit2(&bars.drain[1]);
+      __syncwarp();
+      warp_wait(&bars.drain[1], 0, nullptr, p.status);
     }
   } else if (warp >= KEY_WARP0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kE4M3>::rest));  // (idle)
@@ -628,11 +643,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     const uint32_t to = tmem + lane_base + T_O;
     const uint32_t p_row = sbase + OFF_P + half * P_BYTES;
     const uint32_t p_bar0 = first_cta(&bars.p_full[g][0]), p_bar = p_bar0 + half * 8;
+    const uint32_t s_bar = first_cta(&bars.s_empty[0]);
     auto wait_pv = [&](int t) -> bool {  // the value product of tile t has completed
-      if (!warp_wait<true>(&bars.o_done[t & 1], (t >> 1) & 1, abort, p.status)) return false;
+      if (!warp_wait(&bars.pv_done[t & 1][1], (t >> 1) & 1, abort, p.status)) return false;
       tc_fence_after();
       return true;
     };
+    // 32 scores of the lane; the first `left` of them are of keys the token sees
+    auto load_scores = [](uint32_t taddr, int left, float (&x)[32]) {
+      tmem_ld32(taddr, reinterpret_cast<uint32_t*>(x));
+      tc_wait_ld();
+      if (left < 32) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j >= left) x[j] = -INFINITY;
+      }
+    };
+    const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
     auto publish_m = [&](float m) {  // the running maximum after this group's tile
       bars.m[g][h] = m;  // (both lanes of the head: the same value)
       __syncwarp();
@@ -661,26 +688,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         l = 0.f;
         lm = -INFINITY;
       }
-      if (!warp_wait<true>(&bars.s_full[i % NSB], (i / NSB) & 1, abort, p.status)) break;
+      if (!warp_wait(&bars.s_full[i % NSB], (i / NSB) & 1, abort, p.status)) break;
       tc_fence_after();
-      float x[64];
       const uint32_t ts = tmem + lane_base + T_S + (i % NSB) * (KT / 2);
-      tmem_ld32(ts, reinterpret_cast<uint32_t*>(x));
-      tmem_ld32(ts + 32, reinterpret_cast<uint32_t*>(x) + 32);
-      tc_wait_ld();
-      const int left = lim - jt * KT - half * 64;
-      if (left < 64) {
+      const int left = lim - jt * KT - half * 64;  // keys of this lane's 64 that the token sees
+      float mt = -INFINITY;
+#pragma unroll 1
+      for (int c = 0; c < 64; c += 32) {
+        float x[32];
+        load_scores(ts + c, left - c, x);
+        float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int j = 0; j < 64; ++j)
-          if (j >= left) x[j] = -INFINITY;
+        for (int j = 4; j < 28; j += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[j + e], x[j + 4 + e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[28 + e]);
+        mt = max3(max3(mt, mx[0], mx[1]), mx[2], mx[3]);
       }
-      float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-      for (int j = 4; j < 64; j += 4)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[j + e]);
-      // (log2 units; the scale is positive)
-      float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+      mt *= p.scale_log2;  // log2 units (the scale is positive)
       // The running maximum after tile i - 1, from the other group.  Waited for
       // before this tile's maxima are exchanged: whoever passes the exchange
       // then knows that both lanes' warps of the other group are done with
@@ -721,46 +747,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       }
       // (a row that has seen no key yet has m = -inf: its P is exp2(-inf) = 0)
       const float d = mn == -INFINITY ? 0.f : -mn;
-      uint32_t w[32];
-      float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float e0 = fast_exp2(fmaf(x[2 * j], p.scale_log2, d));
-        const float e1 = fast_exp2(fmaf(x[2 * j + 1], p.scale_log2, d));
-        s0 += e0;
-        s1 += e1;
-        w[j] = pack_bf16x2(e0, e1);
-      }
-      l += s0 + s1;
       // the previous token's output has left TMEM before this one's first
       // value product (the other group writes it out)
       if (first && i > 0 &&
           !warp_wait(&bars.flushed[q4], (nseg - 1) & 1, abort, p.status))
         break;
-      bars.l[g][ln] = l;
       // (an arrival below is for this tile's phase: the group's last one, of
       // tile i - 2, is over once its value product has used the first half)
-      if (i >= 2 && !warp_wait<true>(&bars.p_empty[g][0], ((i - 2) >> 1) & 1, abort, p.status))
-        break;
+      if (i >= 2 && !warp_wait(&bars.pv_done[g][0], ((i - 2) >> 1) & 1, abort, p.status)) break;
+      // The first half's products write all lanes of O: the second half's warps'
+      // lanes are ready, so those products need not wait for their P.
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&bars.l_full[g][q4]);
-        // The first half's products write all lanes of O: these warps' lanes
-        // are ready, so those products need not wait for the second half of P.
-        if (half == 1) mbar_arrive_cluster(p_bar0);
-      }
+      if (half == 1 && lane == 0) mbar_arrive_pair(p_bar0);
       // This half of P has been used by tile i - 1's value product.  (A barrier
       // for each parity of tiles: a group waits on every phase of its own, and
       // one that both waited on could be two phases behind what a wait expects.)
-      if (i > 0 && !warp_wait<true>(&bars.p_empty[g ^ 1][half], ((i - 1) >> 1) & 1, abort, p.status))
+      if (i > 0 && !warp_wait(&bars.pv_done[g ^ 1][half], ((i - 1) >> 1) & 1, abort, p.status))
         break;
+      // (The scores are read from TMEM again, in a rolled loop.  The roles run
+      // different code on the same schedulers: with a lane's 64 scores unrolled
+      // they waited 5.8 cycles an issue for instructions, 6900 cycles a tile.)
+      uint64_t s2 = 0;
+#pragma unroll 1
+      for (int c = 0; c < 64; c += 32) {
+        float x[32];
+        load_scores(ts + c, left - c, x);
+        uint32_t w[16];
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
-        st_shared_v4(p_row + sw128_off(h, c), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        for (int j = 0; j < 16; ++j) {
+          float e0, e1;
+          unpack2(fma2(pack2(x[2 * j], x[2 * j + 1]), scale2, pack2(d, d)), e0, e1);
+          e0 = fast_exp2(e0);
+          e1 = fast_exp2(e1);
+          s2 = add2(s2, pack2(e0, e1));
+          w[j] = pack_bf16x2(e0, e1);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          st_shared_v4(p_row + sw128_off(h, (c >> 3) + k), w[4 * k], w[4 * k + 1], w[4 * k + 2],
+                       w[4 * k + 3]);
+      }
+      {
+        float e0, e1;
+        unpack2(s2, e0, e1);
+        l += e0 + e1;
+      }
+      bars.l[g][ln] = l;
       fence_proxy_async_smem();
+      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(p_bar);
+      if (lane == 0) {
+        mbar_arrive_pair(p_bar);
+        mbar_arrive(&bars.l_full[g][q4]);
+        mbar_arrive_pair(s_bar + (i % NSB) * 8);
+      }
       if (ends) {
         // the segment's end: the sums of both lanes and groups, then this lane's
         // half of O~ / l into the token's output (a token held whole by this
@@ -823,7 +864,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     }
   }
   cluster_sync_all();
-  if (warp == MMA_WARP) {
+  if (warp == S_WARP) {
     tc_fence_after();
     tmem_dealloc2(tmem, TMEM_COLS);
   }
@@ -1111,7 +1152,7 @@ static int launch_value_nb(const __nv_bfloat16* wkv_b, const __nv_bfloat16* omer
 
 template <bool kE4M3>
 static int launch_absorbed(const Params& p, int nc, cudaStream_t st) {
-  alignas(64) CUtensorMap map_qt, map_qr, map_k = {}, map_v = {}, map_1 = {};
+  alignas(64) CUtensorMap map_qt, map_qr, map_k = {}, map_v = {}, map_b = {}, map_1 = {};
   if (int e = bf16_map_3d(&map_qt, p.q_tilde, kC, kH, p.N, kC * 2, kH * kC * 2, 64, HH, 1))
     return e;
   if (int e = bf16_map_3d(&map_qr, p.q_pe, kR, kH, p.N, kR * 2, kH * kR * 2, 64, HH, 1)) return e;
@@ -1119,13 +1160,14 @@ static int launch_absorbed(const Params& p, int nc, cudaStream_t st) {
     // rows as [9 column atoms][rows][64]: a box takes several atoms at once
     const uint64_t rows = p.pool.rows, rb = p.pool.row_stride;
     if (int e = bf16_map_3d(&map_k, p.pool.base, 64, rows, 9, rb, 128, 64, 64, 3)) return e;
-    if (int e = bf16_map_3d(&map_v, p.pool.base, 64, rows, 9, rb, 128, 64, 32, 4)) return e;
+    if (int e = bf16_map_3d(&map_v, p.pool.base, 64, rows, 9, rb, 128, 64, 64, 4)) return e;
+    if (int e = bf16_map_2d(&map_b, p.pool.base, MLA_ROW, rows, rb, 64, p.box ? p.box : 1)) return e;
     if (int e = bf16_map_2d(&map_1, p.pool.base, MLA_ROW, rows, rb, 64, 1)) return e;
   }
   static std::atomic<unsigned long long> attr_done{0};
   if (int e = ensure_smem_attr(absorbed_kernel<kE4M3>, dynamic_smem(), &attr_done)) return e;
   return launch_pdl(absorbed_kernel<kE4M3>, dim3(2 * nc), dim3(NTHREADS), dynamic_smem(), st, p,
-                    map_qt, map_qr, map_k, map_v, map_1);
+                    map_qt, map_qr, map_k, map_v, map_b, map_1);
 }
 
 static int run_absorbed(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const mla_bf16_t* wkv_b,
@@ -1153,7 +1195,8 @@ static int run_absorbed(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const 
   p.pool = pool;
   p.plan = pl;
   p.N = q.N;
-  p.box = pool.page_size % 64 == 0 ? 64 : pool.page_size % 32 == 0 ? 32 : 0;
+  p.box = pool.page_size % 64 == 0 ? 64 : pool.page_size % 32 == 0 ? 32
+          : pool.page_size % 16 == 0 ? 16 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.opart = reinterpret_cast<__nv_bfloat16*>(ws + L.opart);
   p.lse = reinterpret_cast<float*>(ws + L.lse);

@@ -311,11 +311,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm::THREADS, 1)
         const int i = it - lo, buf = i & 1, rb = it / heads;
         const bool fresh = rb != prev;
         const bool last = it + 1 == hi || (it + 1) / heads != rb;
-        ok = warp_wait<true>(&bars.acc_empty[buf], ((i >> 1) & 1) ^ 1, abort, status);
+        ok = warp_wait(&bars.acc_empty[buf], ((i >> 1) & 1) ^ 1, abort, status);
         for (int kc = 0; kc < 8 && ok; ++kc) {
-          if (fresh) ok = warp_wait<true>(&bars.a_full[kc], nblk & 1, abort, status);
+          if (fresh) ok = warp_wait(&bars.a_full[kc], nblk & 1, abort, status);
           const int s = ring % NB;
-          ok = ok && warp_wait<true>(&bars.b_full[s], (ring / NB) & 1, abort, status);
+          ok = ok && warp_wait(&bars.b_full[s], (ring / NB) & 1, abort, status);
           if (!ok) break;
           tc_fence_after();
           const uint32_t al = desc_lo(sbase + kc * CHUNK, 16);
@@ -339,7 +339,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm::THREADS, 1)
       // everything issued so far has finished before TMEM is released
       if (elect_one()) tc_commit2(&bars.drain);
       __syncwarp();
-      warp_wait<true>(&bars.drain, 0, nullptr, status);
+      warp_wait(&bars.drain, 0, nullptr, status);
     }
   } else {
     // ---------------- epilogue: this CTA's 128 rows ----------------
@@ -349,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm::THREADS, 1)
     for (int it = lo; it < hi; ++it) {
       const int i = it - lo, buf = i & 1, rb = it / heads, h = it - rb * heads;
       // (the four warps leave together, so that none waits for another below)
-      if (!all_of_128(warp_wait<true>(&bars.acc_full[buf], (i >> 1) & 1, abort, status))) break;
+      if (!all_of_128(warp_wait(&bars.acc_full[buf], (i >> 1) & 1, abort, status))) break;
       tc_fence_after();
 #pragma unroll 1
       for (int b = 0; b < 4; ++b) {  // keys 0-63, 64-127, values 0-63, 64-127
@@ -360,7 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm::THREADS, 1)
         if (b == 3) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(acc_empty0 + buf * 8);
+          if (lane == 0) mbar_arrive_pair(acc_empty0 + buf * 8);
         }
         // the store before last has read its box
         if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
@@ -435,26 +435,6 @@ struct Bars {
   int abort;
 };
 }  // namespace attn
-
-// pairs of fp32 values in one 64-bit register: one instruction for two
-DEV uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-DEV void unpack2(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-DEV uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 
 __global__ void __launch_bounds__(attn::THREADS, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_constant__ CUtensorMap map_qr,

@@ -4,10 +4,11 @@
 //   O = W_UV[h] (softmax(s) c)
 // Five kernels on the caller's stream:
 //
-//   plan_kernel      one block: each token's sequence and limit, the prefix sum
-//                    of the tokens' 128-key tiles, and its cut into one range
-//                    of equal cost per CTA pair
 //   (fold)           q~ per head, as in mla_decode
+//   plan_kernel      one block, while the fold runs: each token's sequence and
+//                    limit, the prefix sum of the tokens' 128-key tiles, its cut
+//                    into one range of equal cost per CTA pair, and the list of
+//                    tokens that a cut splits
 //   absorbed_kernel  persistent CTA pairs over their ranges
 //   merge_kernel     log-sum-exp merge of the tokens that several pairs held
 //   value_kernel     O = W_UV O~ per head
@@ -35,15 +36,20 @@ struct Plan {
   int32_t* tstart;  // [N + 1] its first tile in the flattened list
   int32_t* tb;      // [nc + 1] first tile of each pair's range
   int32_t* crow;    // [nc + 1] the token that holds that tile
-  int32_t* nact;    // [1] tokens of the sequences (those behind the last one are padding)
+  int32_t* split;   // [nc] pairs after whose range a token is cut for the first time
+  int32_t* nact;    // [2] tokens of the sequences (those behind the last one are padding); entries of split
 };
+
+constexpr int kMaxPairs = 512;
 
 // Every token has at least one tile, so that one that sees nothing still gets
 // its zero output.
 __global__ void __launch_bounds__(1024) plan_kernel(const Seqs q, const Pool pool, const Plan pl,
                                                      int nc) {
   __shared__ int part[1024];
+  __shared__ int tb_s[kMaxPairs + 1], nsplit;
   const int tid = threadIdx.x;
+  pdl_trigger();
   const int nact = min(q.N, q.q0(q.S));
   const int per = (nact + 1023) / 1024;
   const int lo = min(nact, tid * per), hi = min(nact, lo + per);
@@ -84,29 +90,46 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Seqs q, const Pool poo
   }
   const int tot = part[1023];
   for (int r = nact + tid; r <= q.N; r += 1024) pl.tstart[r] = tot;
-  if (tid == 0) *pl.nact = nact;
+  if (tid == 0) {
+    pl.nact[0] = nact;
+    nsplit = 0;
+  }
   __syncthreads();  // tstart, written by the block, is visible to it
   // Cost units: token r spans kTokenCost units of its own, then one per tile,
   // from u(r) = tstart[r] + r * kTokenCost.  Pair c takes the units
   // [c U / nc, (c + 1) U / nc); a range that starts in a token's own units
   // starts at its first tile.
   const long long U = (long long)tot + (long long)nact * kTokenCost;
-  for (int c = tid; c <= nc; c += 1024) {
-    if (c == nc || nact == 0) {
-      pl.tb[c] = tot;
-      pl.crow[c] = nact;
-      continue;
+  int mine = -1;  // the token that holds the first tile of this thread's range (nc < 1024)
+  if (tid <= nc) {
+    const int c = tid;
+    int t = tot, b = nact;
+    if (c < nc && nact > 0) {
+      const long long u = (long long)c * U / nc;
+      int a = 0, e = nact;  // u(a) <= u < u(e)
+      while (e - a > 1) {
+        const int m = (a + e) >> 1;
+        if ((long long)pl.tstart[m] + (long long)m * kTokenCost <= u) a = m; else e = m;
+      }
+      const long long into = u - ((long long)pl.tstart[a] + (long long)a * kTokenCost);
+      t = pl.tstart[a] + (into > kTokenCost ? (int)(into - kTokenCost) : 0);
+      b = a;
+      mine = a;
     }
-    const long long u = (long long)c * U / nc;
-    int a = 0, e = nact;  // u(a) <= u < u(e)
-    while (e - a > 1) {
-      const int m = (a + e) >> 1;
-      if ((long long)pl.tstart[m] + (long long)m * kTokenCost <= u) a = m; else e = m;
-    }
-    const long long into = u - ((long long)pl.tstart[a] + (long long)a * kTokenCost);
-    pl.tb[c] = pl.tstart[a] + (into > kTokenCost ? (int)(into - kTokenCost) : 0);
-    pl.crow[c] = a;
+    pl.tb[c] = tb_s[c] = t;
+    pl.crow[c] = b;
   }
+  __syncthreads();
+  // boundary c cuts its token, and no earlier one does (the order of the list
+  // changes nothing but the order of the merge's work)
+  if (mine >= 0 && tid > 0) {
+    const int rs = pl.tstart[mine];
+    if (rs < tb_s[tid] && tb_s[tid - 1] <= rs) pl.split[atomicAdd(&nsplit, 1)] = tid;
+  }
+  __syncthreads();
+  if (tid == 0) pl.nact[1] = nsplit;
+  // the fold before this kernel has finished too when it has
+  pdl_wait();
 }
 
 // ===========================================================================
@@ -250,7 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   }
   const uint32_t rank = cluster_ctarank();
   const int cid = blockIdx.x >> 1;
-  // (the plan was complete before the fold kernel began)
+  pdl_wait();  // the plan, and the fold before it
   const int t_begin = ld_global_nc_s32_early(p.plan.tb + cid);
   const int n = ld_global_nc_s32_early(p.plan.tb + cid + 1) - t_begin;
   const int bb0 = min(ld_global_nc_s32_early(p.plan.crow + cid), p.N - 1);
@@ -527,7 +550,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   } else if (warp == Q_WARP) {
     // ---------------- queries: this CTA's 64 heads of each token ----------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kE4M3>::rest));
-    pdl_wait();  // q~ is the fold kernel's output (the other roles read only inputs and the plan)
     const uint32_t bar = first_cta(&bars.q_full);
     int bb = bb0, i = 0;
     for (int seg = 0; i < n; ++seg, ++bb) {
@@ -873,106 +895,118 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 
 // ===========================================================================
 // merge: O~ = sum_s 2^(lse_s - max) O~_s / sum_s 2^(lse_s - max) over the
-// segments of a token that several pairs held.  Grid (range boundaries
-// 1 .. pairs-1, heads); boundary c serves the token it falls inside when it is
-// the token's first one.  256 threads: 64 16-byte chunks of the head's latent,
-// four threads each over every fourth segment.
+// segments of the tokens that several pairs held (the plan's list).  A unit of
+// work is a token and eight heads, or two when few tokens are split (then each
+// has many segments); 256 threads: a head's 64 16-byte chunks, four threads
+// for each chunk's segments (or four heads at once).  Bound by latency: three
+// dependent loads before the partial outputs, 2 x 1 KB a head and segment.
+// (A block for each boundary and head, most of them with nothing to do, took
+// 25 us where this takes 6.)
 // ===========================================================================
-constexpr int kMaxPairs = 512;
-
 __global__ void __launch_bounds__(256) merge_kernel(const __nv_bfloat16* __restrict__ opart,
                                                      const float* __restrict__ lse, const Plan pl,
                                                      int nc, __nv_bfloat16* __restrict__ omerged) {
-  __shared__ float w[kMaxPairs];
   __shared__ int slots[kMaxPairs];
   __shared__ int count;
+  __shared__ float w[4][kMaxPairs], wsum[4];
   __shared__ float acc_s[3][64][8];
-  __shared__ float wsum;
-  const int cb = blockIdx.x + 1, h = blockIdx.y, tid = threadIdx.x;
+  const int tid = threadIdx.x, ch = tid & 63, g = tid >> 6;
   pdl_trigger();
   // every block waits, those with nothing to merge too: the value kernel
   // relies on this grid's completion implying the attend kernel's
   pdl_wait();
-  const int t = ld_global_nc_s32_early(pl.tb + cb);
-  const int b = ld_global_nc_s32_early(pl.crow + cb);
-  if (b >= ld_global_nc_s32_early(pl.nact)) return;
-  const int rs = ld_global_nc_s32_early(pl.tstart + b);
-  const int re = ld_global_nc_s32_early(pl.tstart + b + 1);
-  const int before = ld_global_nc_s32_early(pl.tb + cb - 1);
-  if (rs == t || before > rs) return;
-  // segments in pair order: slot 1 of pair cb - 1 (slot 0 when the token
-  // starts its range), slot 0 of every later pair whose range starts inside
-  // the token and is not empty
-  if (tid < 32) {
-    int have = 1;
-    if (tid == 0) slots[0] = 2 * (cb - 1) + (rs > before ? 1 : 0);
-    for (int c0 = cb; c0 < nc; c0 += 32) {
-      const int c = c0 + tid;
-      const int a = c < nc ? ld_global_nc_s32_early(pl.tb + c) : re;
-      const int e = c < nc ? ld_global_nc_s32_early(pl.tb + c + 1) : re;
-      const bool in = a < re && e > a;
-      const unsigned m = __ballot_sync(0xffffffffu, in);
-      const int at = have + __popc(m & ((1u << tid) - 1u));
-      if (in) slots[at] = 2 * c;
-      have += __popc(m);
-      if (!__any_sync(0xffffffffu, a < re)) break;
+  const int nsplit = ld_global_nc_s32_early(pl.nact + 1);
+  const bool many = nsplit >= 16;  // four heads at once, each thread all segments
+  const int per = many ? 8 : 2;    // heads of a unit
+  const int units = nsplit * (kH / per);
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const int cb = ld_global_nc_s32_early(pl.split + u / (kH / per));
+    const int h0 = u % (kH / per) * per;
+    const int b = ld_global_nc_s32_early(pl.crow + cb);
+    // segments in pair order: slot 1 of pair cb - 1 (slot 0 when the token
+    // starts its range), slot 0 of every later pair whose range starts inside
+    // the token and is not empty
+    if (tid < 32) {
+      const int rs = ld_global_nc_s32_early(pl.tstart + b);
+      const int re = ld_global_nc_s32_early(pl.tstart + b + 1);
+      int have = 1;
+      if (tid == 0)
+        slots[0] = 2 * (cb - 1) + (rs > ld_global_nc_s32_early(pl.tb + cb - 1) ? 1 : 0);
+      for (int c0 = cb; c0 < nc; c0 += 32) {
+        const int c = c0 + tid;
+        const int a = c < nc ? ld_global_nc_s32_early(pl.tb + c) : re;
+        const int e = c < nc ? ld_global_nc_s32_early(pl.tb + c + 1) : re;
+        const bool in = a < re && e > a;
+        const unsigned m = __ballot_sync(0xffffffffu, in);
+        if (in) slots[have + __popc(m & ((1u << tid) - 1u))] = 2 * c;
+        have += __popc(m);
+        if (!__all_sync(0xffffffffu, a < re)) break;
+      }
+      if (tid == 0) count = have;
     }
-    __syncwarp();
-    float mx = -INFINITY;
-    for (int i = tid; i < have; i += 32) {
-      const float l = lse[(size_t)slots[i] * kH + h];
-      w[i] = l;
-      mx = fmaxf(mx, l);  // (drops a NaN, which the weights below keep)
-    }
+    __syncthreads();
+    const int n = count;
+    for (int hh = 0; hh < per; hh += many ? 4 : 1) {
+      const int q = many ? g : 0;  // which of the heads at once
+      const int h = h0 + hh + q;
+      // weights: a warp for each head at once
+      if ((tid & 63) < 32 && (many || g == 0)) {
+        const int ln = tid & 31;
+        float mx = -INFINITY;
+        for (int i = ln; i < n; i += 32) {
+          const float l = lse[(size_t)slots[i] * kH + h];
+          w[q][i] = l;
+          mx = fmaxf(mx, l);  // (drops a NaN, which the weights below keep)
+        }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    float s = 0.f;
-    for (int i = tid; i < have; i += 32) {
-      const float e = w[i] == -INFINITY ? 0.f : exp2f(w[i] - mx);
-      w[i] = e;
-      s += e;
-    }
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        float sum = 0.f;
+        for (int i = ln; i < n; i += 32) {
+          const float e = w[q][i] == -INFINITY ? 0.f : exp2f(w[q][i] - mx);
+          w[q][i] = e;
+          sum += e;
+        }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (tid == 0) {
-      count = have;
-      wsum = s;
-    }
-  }
-  __syncthreads();
-  const int n = count;
-  const int ch = tid & 63, g = tid >> 6;
-  const __nv_bfloat16* src = opart + (size_t)h * kC + ch * 8;
-  float acc[8];
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (ln == 0) wsum[q] = sum;
+      }
+      __syncthreads();
+      const __nv_bfloat16* src = opart + (size_t)h * kC + ch * 8;
+      float acc[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+      for (int e = 0; e < 8; ++e) acc[e] = 0.f;
 #pragma unroll 4
-  for (int i = g; i < n; i += 4) {
-    const uint4 v = ld_global_nc_v4(src + (size_t)slots[i] * kH * kC);
-    const float wi = w[i];
-    const __nv_bfloat162* pv = reinterpret_cast<const __nv_bfloat162*>(&v);
+      for (int i = many ? 0 : g; i < n; i += many ? 1 : 4) {
+        const uint4 v = ld_global_nc_v4(src + (size_t)slots[i] * kH * kC);
+        const float wi = w[q][i];
+        const __nv_bfloat162* pv = reinterpret_cast<const __nv_bfloat162*>(&v);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = __bfloat1622float2(pv[e]);
-      acc[2 * e] += wi * f.x;
-      acc[2 * e + 1] += wi * f.y;
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = __bfloat1622float2(pv[e]);
+          acc[2 * e] += wi * f.x;
+          acc[2 * e + 1] += wi * f.y;
+        }
+      }
+      if (!many) {
+        if (g > 0)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc_s[g - 1][ch][e] = acc[e];
+        __syncthreads();
+        if (g == 0)
+          for (int k = 0; k < 3; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] += acc_s[k][ch][e];
+      }
+      if (many || g == 0) {
+        const float inv = wsum[q] == 0.f ? 0.f : 1.f / wsum[q];
+        *reinterpret_cast<uint4*>(omerged + ((size_t)b * kH + h) * kC + ch * 8) =
+            make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv),
+                       pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                       pack_bf16x2(acc[4] * inv, acc[5] * inv),
+                       pack_bf16x2(acc[6] * inv, acc[7] * inv));
+      }
+      __syncthreads();  // w, acc_s and slots may be written again
     }
-  }
-  if (g > 0)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc_s[g - 1][ch][e] = acc[e];
-  __syncthreads();
-  if (g == 0) {
-    for (int k = 0; k < 3; ++k)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += acc_s[k][ch][e];
-    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
-    uint4 o;
-    o.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    o.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-    o.z = pack_bf16x2(acc[4] * inv, acc[5] * inv);
-    o.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
-    *reinterpret_cast<uint4*>(omerged + ((size_t)b * kH + h) * kC + ch * 8) = o;
   }
 }
 
@@ -1117,7 +1151,7 @@ static int max_pairs() {
 }
 
 struct AbsorbedWs {
-  size_t q_tilde, opart, lse, omerged, seq, lim, tstart, tb, crow, nact, total;
+  size_t q_tilde, opart, lse, omerged, seq, lim, tstart, tb, crow, split, nact, total;
 };
 
 static AbsorbedWs absorbed_ws(int N, int nc) {
@@ -1131,7 +1165,8 @@ static AbsorbedWs absorbed_ws(int N, int nc) {
   w.tstart = round_up(w.lim + (size_t)N * 4, 256);
   w.tb = round_up(w.tstart + (size_t)(N + 1) * 4, 256);
   w.crow = round_up(w.tb + (size_t)(nc + 1) * 4, 256);
-  w.nact = round_up(w.crow + (size_t)(nc + 1) * 4, 256);
+  w.split = round_up(w.crow + (size_t)(nc + 1) * 4, 256);
+  w.nact = round_up(w.split + (size_t)nc * 4, 256);
   w.total = w.nact + 256;
   return w;
 }
@@ -1181,14 +1216,14 @@ static int run_absorbed(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const 
   pl.tstart = reinterpret_cast<int32_t*>(ws + L.tstart);
   pl.tb = reinterpret_cast<int32_t*>(ws + L.tb);
   pl.crow = reinterpret_cast<int32_t*>(ws + L.crow);
+  pl.split = reinterpret_cast<int32_t*>(ws + L.split);
   pl.nact = reinterpret_cast<int32_t*>(ws + L.nact);
   __nv_bfloat16* q_tilde = reinterpret_cast<__nv_bfloat16*>(ws + L.q_tilde);
-  // plain launch: complete before the fold starts, so the attend kernel, which
-  // may start during the fold, finds the plan
-  plan_kernel<<<1, 1024, 0, st>>>(q, pool, pl, nc);
-  if (int e = launch_status()) return e;
+  // The fold waits for the stream's earlier work as usual; the others may start
+  // while their predecessor drains.
   if (int e = mla_fold_wuk(q_nope, wkv_b, q.N, reinterpret_cast<mla_bf16_t*>(q_tilde), st))
     return e;
+  if (int e = launch_pdl(plan_kernel, dim3(1), dim3(1024), 0, st, q, pool, pl, nc)) return e;
   Params p;
   p.q_tilde = q_tilde;
   p.q_pe = reinterpret_cast<const __nv_bfloat16*>(q_pe);
@@ -1206,7 +1241,7 @@ static int run_absorbed(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const 
                                          : launch_absorbed<false>(p, nc, st))
     return e;
   if (nc > 1)
-    if (int e = launch_pdl(merge_kernel, dim3(nc - 1, kH), dim3(256), 0, st,
+    if (int e = launch_pdl(merge_kernel, dim3(8 * nc), dim3(256), 0, st,
                            (const __nv_bfloat16*)p.opart, (const float*)p.lse, pl, nc, p.omerged))
       return e;
   const __nv_bfloat16* w = reinterpret_cast<const __nv_bfloat16*>(wkv_b);

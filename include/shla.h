@@ -398,10 +398,12 @@ int mla_query_proj(const mla_bf16_t* x, const mla_bf16_t* wq_a, const mla_bf16_t
  *          skipped and counted in status[1].  Slots are distinct: of a slot
  *          listed twice, each 16-byte piece holds one of the two rows'.
  * The scale of a group is the least power of two 2^n, -117 <= n <= 119, with
- * max |x| <= 448 * 2^n over the group's finite values; a code is x / scale
- * (exact) rounded to nearest even, saturated at 448.  An infinity or NaN is
- * stored as NaN.  A power of two makes code * scale exact in bf16, so the
- * rounding to a code is the only one.  N >= 0.
+ * max |x| <= 448 * 2^n over the group; a code is x / scale (exact) rounded to
+ * nearest even, saturated at 448.  A group with an infinity or NaN gets the
+ * scale NaN and codes 0: all its values read as NaN.  A power of two makes code
+ * * scale exact in bf16, so the rounding to a code is the only one.  (Rows
+ * written by other means keep to this: scales 2^n in that range or NaN, no NaN
+ * codes 0x7f, 0xff.)  N >= 0.
  *
  * mla_page_read returns the rows of slots as bf16 [N] rows (exactly code *
  * scale); slot -1, and any other slot outside the pool (counted in

@@ -163,7 +163,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Seqs q, const Pool poo
 // moves them at 23 bytes a cycle while the SM's other shared-memory accesses
 // wait: 3600 cycles.)
 //
-// Roles (640 threads a CTA):
+// Roles (640 threads a CTA; 896 for 8-bit pages, which have eight warps for keys
+// and eight for values):
 //   warps 0-7    softmax, two groups of four warps that take every other tile, a
 //                lane of TMEM per thread.  The running maximum goes from group
 //                to group (published as soon as a tile's is known, before its
@@ -171,18 +172,14 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Seqs q, const Pool poo
 //   warps 8-11   keys; 12-15 values.  16-bit pages: a warp for each chunk, TMA (one
 //                warp for all chunks took 700 cycles for each, in turn).  8-bit:
 //                loads, exact conversion to bf16 and swizzled stores.
-//   warp 16      issues the score products (first CTA), TMEM owner
-//   warp 17      queries (TMA)
-//   warp 18      issues the value products (first CTA).  One warp for both spent
-//                4400 cycles a tile in barrier tests and issues.
+//   then one warp each that issues the score products (first CTA; TMEM owner),
+//                loads queries (TMA), and issues the value products (first CTA)
 // TMEM (512 columns): four score tiles [0,256), output [256,512).
 // ===========================================================================
 
 constexpr int HH = kH / 2;             // heads of a CTA
 constexpr int NSB = 4;                 // score tiles in TMEM (64 columns each)
 constexpr int NKC = 3;                 // chunks of a tile's keys (192 columns); values: two of 64 keys
-constexpr int KEY_WARP0 = 8, VAL_WARP0 = 12, S_WARP = 16, Q_WARP = 17, O_WARP = 18;
-constexpr int NTHREADS = 640;
 constexpr int Q_ATOM = HH * 128;       // 64 columns of 64 rows, 128 B swizzle
 constexpr int K_ATOM = KT / 2 * 128;   // 64 columns of this CTA's 64 keys
 constexpr int V_ATOM = 64 * 128;       // 64 columns of a chunk's 64 keys
@@ -196,11 +193,16 @@ constexpr uint32_t T_S = 0, T_O = 256, TMEM_COLS = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 static_assert(OFF_K % 1024 == 0 && OFF_V % 1024 == 0 && OFF_P % 1024 == 0, "alignment");
 static_assert(T_S + NSB * KT / 2 <= T_O, "TMEM plan");
-// registers: 96 a thread at launch, five groups of four warps
+constexpr int KEY_WARP0 = 8;
 template <bool kE4M3>
-struct Regs {
-  static constexpr int soft = kE4M3 ? 120 : 128, load = kE4M3 ? 88 : 80, rest = 64;
-  static_assert(2 * soft + 2 * load + rest <= 5 * 96, "register split");
+struct Roles {
+  static constexpr int load_warps = kE4M3 ? 8 : 4;  // of keys, and of values
+  static constexpr int val0 = KEY_WARP0 + load_warps, s = val0 + load_warps, q = s + 1, o = s + 2;
+  static constexpr int threads = 32 * (s + 4);
+  // registers: an equal share at launch, then by role (in groups of four warps)
+  static constexpr int groups = threads / 128, share = 65536 / threads / 8 * 8;
+  static constexpr int soft = kE4M3 ? 80 : 128, load = kE4M3 ? 72 : 80, rest = kE4M3 ? 56 : 64;
+  static_assert(2 * soft + load_warps / 2 * load + rest <= groups * share, "register split");
 };
 
 struct Params {
@@ -254,13 +256,14 @@ struct Pos {
 };
 
 template <bool kE4M3>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::threads, 1)
     absorbed_kernel(const Params p, const __grid_constant__ CUtensorMap map_qt,
                     const __grid_constant__ CUtensorMap map_qr,
                     const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v,
                     const __grid_constant__ CUtensorMap map_b,
                     const __grid_constant__ CUtensorMap map_1) {
+  using R = Roles<kE4M3>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   __shared__ Bars bars;
@@ -291,9 +294,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   // a barrier of the pair's first CTA
   auto first_cta = [&](uint64_t* bar) { return mapa_shared(smem_u32(bar), 0); };
 
-  if (warp == S_WARP) tmem_alloc2(&bars.tmem_base, TMEM_COLS);
+  if (warp == R::s) tmem_alloc2(&bars.tmem_base, TMEM_COLS);
   if (tid == 0) {
-    constexpr int fill = kE4M3 ? 8 : 1;  // four warps of each CTA, or one arrival and bytes
+    constexpr int fill = kE4M3 ? 2 * Roles<true>::load_warps : 1;  // warps of both CTAs, or one arrival and bytes
     mbar_init(&bars.q_full, 1);
     mbar_init(&bars.q_free, 1);
     for (int i = 0; i < NKC; ++i) {
@@ -330,11 +333,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 
   if (n <= 0) {
     // an empty range (fewer tiles than pairs): nothing to do
-  } else if (warp >= KEY_WARP0 && warp < S_WARP) {
+  } else if (warp >= KEY_WARP0 && warp < R::s) {
     // ---------------- keys and values ----------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kE4M3>::load));
-    const bool val = warp >= VAL_WARP0;
-    const int w4 = warp & 3;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::load));
+    const bool val = warp >= R::val0;
+    const int wl = warp - (val ? R::val0 : KEY_WARP0);
     int bb = bb0, jt = jt0 - 1, nr = tiles_of(bb0), lim = 0, bad = 0;
     const int32_t* trow = nullptr;
     bool last = false;  // the token sees all its sequence's positions: count its bad pages
@@ -361,7 +364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     };
     enter();
     if constexpr (!kE4M3) {
-      const int chunk = w4;  // of the keys' columns, or of the values' keys
+      const int chunk = wl;  // of the keys' columns, or of the values' keys
       if (chunk < (val ? 2 : NKC)) {
         const int sub = val ? chunk * 64 : rank * 64;  // this chunk's first key in a tile
         uint64_t* const full = val ? &bars.v_full[chunk] : &bars.k_full[chunk];
@@ -429,10 +432,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         }
       }
     } else {
-      // 8-bit: steps of 512 units of 16 codes, four a thread of the four warps,
-      // the next step's loads issued before this one's conversion.  Keys: 16
-      // rows of 32 units a step (and one 16-byte piece of a rotary key a
-      // thread); values: 32 rows (a chunk) of 16 units.
+      // 8-bit: a tile in two steps of 1024 units of 16 codes, four a thread.  Keys:
+      // 32 rows of 32 units a step (and one 16-byte piece of a rotary key a
+      // thread); values: 64 rows (half of the keys) of 16 units.  The next step's
+      // loads are in flight while this one's codes are converted: 36 KB an SM.
       // Groups of 32 keys: two a tile for keys (this CTA's 64), four for values.
       // Lane l looks up the page of each group's l-th key, a tile ahead: r[g] is
       // its pool row for the current tile, pg[g] its page for the next.
@@ -450,96 +453,89 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       auto enter_tile = [&](bool more) {  // the fetched tile becomes the current one
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
+          if (g >= groups) break;
           const int k = jt * KT + sub + g * 32 + lane;
           r[g] = row_at(pg[g], k % p.pool.page_size,
-                        val && rank == 0 && w4 == 0 && last && k < lim);
+                        val && rank == 0 && wl == 0 && last && k < lim);
         }
         if (more) fetch();
       };
       fetch();
-      uint4 code[4], rope, ncode[4], nrope;
-      float sc[4], nsc[4];
-      const int ch = val ? lane & 15 : lane;
-      const int ugrp = val ? rank * 2 + (ch >> 3) : lane >> 3;   // its scale
-      const int uoff = val ? rank * 256 + ch * 16 : lane * 16;   // its codes
-      // row within the 32-key group of unit `it` of step half `st`
-      auto unit_row = [&](int st, int it) {
-        return val ? w4 * 8 + it * 2 + (lane >> 4) : st * 16 + w4 * 4 + it;
-      };
-      auto load = [&](int st, int rows) {  // rows: the group's pool rows
+      uint4 code[4], rope = make_uint4(0, 0, 0, 0);
+      float sc[4];
+      const int ch = val ? lane & 15 : lane;                    // unit of a row
+      const int soff = pages::kScaleOff + (val ? rank * 2 + (ch >> 3) : lane >> 3) * 4;
+      const int uoff = val ? rank * 256 + ch * 16 : lane * 16;
+      // row of this thread's unit `it` in the step
+      const int row0 = val ? wl * 8 + (lane >> 4) : wl * 4, row_it = val ? 2 : 1;
+      auto load = [&](int st) {
+        // (a warp's rows lie in one group)
+        const int rows = !val ? (st ? r[1] : r[0])
+                         : wl < 4 ? (st ? r[2] : r[0]) : (st ? r[3] : r[1]);
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
-          const int y = __shfl_sync(0xffffffffu, rows, unit_row(st, it));
-          ncode[it] = make_uint4(0, 0, 0, 0);
-          nsc[it] = 1.f;
+          const int y = __shfl_sync(0xffffffffu, rows, (row0 + it * row_it) & 31);
+          code[it] = make_uint4(0, 0, 0, 0);
+          sc[it] = 1.f;
           if (y < p.pool.rows) {
             const uint8_t* src = p.pool.base + (long long)y * p.pool.row_stride;
-            ncode[it] = ld_global_nc_v4(src + uoff);
-            nsc[it] = u2f((uint32_t)ld_global_nc_s32_early(
-                reinterpret_cast<const int32_t*>(src + pages::kScaleOff + ugrp * 4)));
+            code[it] = ld_global_nc_v4(src + uoff);
+            sc[it] = u2f((uint32_t)ld_global_nc_s32_early(reinterpret_cast<const int32_t*>(src + soff)));
           }
         }
         if (!val) {
-          const int y = __shfl_sync(0xffffffffu, rows, st * 16 + w4 * 4 + (lane >> 3));
-          nrope = make_uint4(0, 0, 0, 0);
+          const int y = __shfl_sync(0xffffffffu, rows, wl * 4 + (lane >> 3));
+          rope = make_uint4(0, 0, 0, 0);
           if (y < p.pool.rows)
-            nrope = ld_global_nc_v4(p.pool.base + (long long)y * p.pool.row_stride +
-                                    pages::kRopeOff + (lane & 7) * 16);
+            rope = ld_global_nc_v4(p.pool.base + (long long)y * p.pool.row_stride +
+                                   pages::kRopeOff + (lane & 7) * 16);
         }
       };
       const uint32_t full0 = first_cta(val ? &bars.v_full[0] : &bars.k_full[0]);
+      const uint32_t atom0 =
+          val ? sbase + OFF_V + (ch >> 2) * V_ATOM : sbase + OFF_K + (lane >> 2) * K_ATOM;
+      const int c2 = (ch & 3) * 2;
       bool ok = true;
       enter_tile(n > 1);
-      load(0, r[0]);
+      load(0);
 #pragma unroll 1
-      for (int i = 0; i < n && ok; ++i) {
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+      for (int q = 0; q < 2 * n; ++q) {
+        const int i = q >> 1, st = q & 1;
+        if (val) {
+          if (i > 0)
+            ok = warp_wait(&bars.pv_done[(i - 1) & 1][st], ((i - 1) >> 1) & 1, abort, p.status);
+        } else if (st == 0) {
+          // (the last chunk's products are the last to finish)
+          ok = warp_wait(&bars.k_empty[NKC - 1], (i & 1) ^ 1, abort, p.status);
+        }
+        if (!ok) break;
+        const uint32_t atom = atom0 + (val ? st * V_CHUNK : 0);
+        const int rbase = row0 + (val ? 0 : st * 32);
+        const bool big = pages::any_big(sc);
 #pragma unroll
-          for (int it = 0; it < 4; ++it) {
-            code[it] = ncode[it];
-            sc[it] = nsc[it];
-          }
-          rope = nrope;
-          if (c < 3) {
-            const int g = val ? c + 1 : (c + 1) >> 1;
-            load((c + 1) & 1, g == 0 ? r[0] : g == 1 ? r[1] : g == 2 ? r[2] : r[3]);
-          } else if (i + 1 < n) {
-            enter_tile(i + 2 < n);
-            load(0, r[0]);
-          }
-          // (keys: the last chunk's products are the last to finish)
-          if (!val) {
-            if (c == 0) ok = warp_wait(&bars.k_empty[NKC - 1], (i & 1) ^ 1, abort, p.status);
-          } else if (i > 0 && (c & 1) == 0 && ok) {
-            ok = warp_wait(&bars.pv_done[(i - 1) & 1][c >> 1], ((i - 1) >> 1) & 1, abort,
-                           p.status);
-          }
-          if (!ok) break;
-          const uint32_t atom = val ? sbase + OFF_V + (c >> 1) * V_CHUNK + (ch >> 2) * V_ATOM
-                                    : sbase + OFF_K + (lane >> 2) * K_ATOM;
-          const int c2 = (ch & 3) * 2;
-#pragma unroll
-          for (int it = 0; it < 4; ++it) {
-            const int row = unit_row(c & 1, it) + (val ? c & 1 : c >> 1) * 32;
-            uint4 o0, o1;
-            pages::dequant16(code[it], sc[it], o0, o1);
-            st_shared_v4(atom + sw128_off(row, c2), o0.x, o0.y, o0.z, o0.w);
-            st_shared_v4(atom + sw128_off(row, c2 + 1), o1.x, o1.y, o1.z, o1.w);
-          }
-          if (!val)
-            st_shared_v4(sbase + OFF_K + 8 * K_ATOM +
-                             sw128_off(c * 16 + w4 * 4 + (lane >> 3), lane & 7),
-                         rope.x, rope.y, rope.z, rope.w);
-          if (val ? (c & 1) : c == 3) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (val) {
-                mbar_arrive_pair(full0 + (c >> 1) * 8);
-              } else {
-                for (int k = 0; k < NKC; ++k) mbar_arrive_pair(full0 + k * 8);
-              }
+        for (int it = 0; it < 4; ++it) {
+          const int row = rbase + it * row_it;
+          uint4 o0, o1;
+          pages::dequant16(code[it], sc[it], big, o0, o1);
+          st_shared_v4(atom + sw128_off(row, c2), o0.x, o0.y, o0.z, o0.w);
+          st_shared_v4(atom + sw128_off(row, c2 + 1), o1.x, o1.y, o1.z, o1.w);
+        }
+        if (!val)
+          st_shared_v4(sbase + OFF_K + 8 * K_ATOM +
+                           sw128_off(st * 32 + wl * 4 + (lane >> 3), lane & 7),
+                       rope.x, rope.y, rope.z, rope.w);
+        if (q + 1 < 2 * n) {
+          if (st == 1) enter_tile(i + 2 < n);
+          load(st ^ 1);
+        }
+        if (val || st == 1) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (val) {
+              mbar_arrive_pair(full0 + st * 8);
+            } else {
+              for (int k = 0; k < NKC; ++k) mbar_arrive_pair(full0 + k * 8);
             }
           }
         }
@@ -547,9 +543,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     }
     bad = __reduce_add_sync(0xffffffffu, bad);
     if (lane == 0 && bad && p.status) atomicAdd(p.status + 1, bad);
-  } else if (warp == Q_WARP) {
+  } else if (warp == R::q) {
     // ---------------- queries: this CTA's 64 heads of each token ----------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kE4M3>::rest));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::rest));
     const uint32_t bar = first_cta(&bars.q_full);
     int bb = bb0, i = 0;
     for (int seg = 0; i < n; ++seg, ++bb) {
@@ -563,9 +559,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       __syncwarp();
       i += tiles_of(bb) - (seg == 0 ? jt0 : 0);
     }
-  } else if (warp == S_WARP) {
+  } else if (warp == R::s) {
     // ---------------- score products ----------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kE4M3>::rest));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::rest));
     if (rank == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(128, KT, 0, 0);
       constexpr uint32_t hi128 = desc_hi(1024, kSwizzle128B);
@@ -612,9 +608,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       __syncwarp();
       warp_wait(&bars.drain[0], 0, nullptr, p.status);
     }
-  } else if (warp == O_WARP) {
+  } else if (warp == R::o) {
     // ---------------- value products ----------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kE4M3>::rest));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::rest));
     if (rank == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(128, 256, 0, 1);
       constexpr uint32_t hi128 = desc_hi(1024, kSwizzle128B);
@@ -653,9 +649,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       warp_wait(&bars.drain[1], 0, nullptr, p.status);
     }
   } else if (warp >= KEY_WARP0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kE4M3>::rest));  // (idle)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::rest));  // (idle)
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<kE4M3>::soft));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::soft));
     // ---------------- softmax: group g = tiles i with i % 2 == g ----------------
     // Thread = TMEM lane: head h = lane % 64 of this CTA's, keys (and latent
     // columns) of half lane / 64.
@@ -886,7 +882,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     }
   }
   cluster_sync_all();
-  if (warp == S_WARP) {
+  if (warp == R::s) {
     tc_fence_after();
     tmem_dealloc2(tmem, TMEM_COLS);
   }
@@ -1130,13 +1126,14 @@ static int max_pairs() {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(2 * kMaxPairs);
-  cfg.blockDim = dim3(NTHREADS);
+  cfg.blockDim = dim3(Roles<true>::threads);
   cfg.dynamicSmemBytes = dynamic_smem();
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaFuncSetAttribute(absorbed_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  // (one CTA an SM either way: shared memory)
+  if (cudaFuncSetAttribute(absorbed_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            dynamic_smem()) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, absorbed_kernel<false>, &cfg) != cudaSuccess || n < 1) {
+      cudaOccupancyMaxActiveClusters(&n, absorbed_kernel<true>, &cfg) != cudaSuccess || n < 1) {
     cudaGetLastError();
     int sms = 148;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
@@ -1201,7 +1198,7 @@ static int launch_absorbed(const Params& p, int nc, cudaStream_t st) {
   }
   static std::atomic<unsigned long long> attr_done{0};
   if (int e = ensure_smem_attr(absorbed_kernel<kE4M3>, dynamic_smem(), &attr_done)) return e;
-  return launch_pdl(absorbed_kernel<kE4M3>, dim3(2 * nc), dim3(NTHREADS), dynamic_smem(), st, p,
+  return launch_pdl(absorbed_kernel<kE4M3>, dim3(2 * nc), dim3(Roles<kE4M3>::threads), dynamic_smem(), st, p,
                     map_qt, map_qr, map_k, map_v, map_b, map_1);
 }
 

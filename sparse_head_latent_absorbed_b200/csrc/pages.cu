@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(256) page_write_kernel(
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   float x[16];
   float top = 0.f;
+  bool finite = true;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     x[2 * i] = __uint_as_float(w[i] << 16);
@@ -45,12 +46,13 @@ __global__ void __launch_bounds__(256) page_write_kernel(
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    // infinities become NaN and, like NaN, do not count towards the scale
-    if (!(fabsf(x[i]) <= 3.4e38f)) x[i] = __uint_as_float(0x7fc00000u);
     top = fmaxf(top, fabsf(x[i]));  // (fmaxf drops a NaN)
+    finite = finite && fabsf(x[i]) <= 3.4e38f;
   }
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  // a group with a NaN or an infinity: scale NaN, codes 0
+  const unsigned bad = __ballot_sync(0xffffffffu, !finite) >> (lane & 24) & 0xffu;
   const int n = scale_exponent(top);
   const float inv = pow2(-n);
   uint32_t c[4];
@@ -58,8 +60,11 @@ __global__ void __launch_bounds__(256) page_write_kernel(
   for (int i = 0; i < 4; ++i)
     c[i] = to_e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) |
            (to_e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
-  *reinterpret_cast<uint4*>(dst + lane * 16) = make_uint4(c[0], c[1], c[2], c[3]);
-  if ((lane & 7) == 0) *reinterpret_cast<float*>(dst + kScaleOff + (lane >> 3) * 4) = pow2(n);
+  *reinterpret_cast<uint4*>(dst + lane * 16) =
+      bad ? make_uint4(0, 0, 0, 0) : make_uint4(c[0], c[1], c[2], c[3]);
+  if ((lane & 7) == 0)
+    *reinterpret_cast<float*>(dst + kScaleOff + (lane >> 3) * 4) =
+        bad ? __uint_as_float(0x7fc00000u) : pow2(n);
   if (lane < 8) *reinterpret_cast<uint4*>(dst + kRopeOff + lane * 16) = pe;
 }
 
@@ -85,7 +90,7 @@ __global__ void __launch_bounds__(256) page_read_kernel(
           __int_as_float(ld_global_nc_s32_early(reinterpret_cast<const int32_t*>(
               src + kScaleOff + (lane >> 3) * 4)));
       if (lane < 8) pe = ld_global_nc_v4(src + kRopeOff + lane * 16);
-      dequant16(c, s, a, b);
+      dequant16(c, s, __any_sync(0xffffffffu, s > 128.f), a, b);
     } else {
       a = ld_global_nc_v4(src + lane * 32);
       b = ld_global_nc_v4(src + lane * 32 + 16);

@@ -64,42 +64,50 @@ DEV float2 from_e4m3x2(uint32_t codes) {
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
-// Four codes times 2^n as four bf16 values, exactly: a code's sign, exponent
-// and mantissa bits moved into bf16's places read as value * 2^-120 (bf16
-// subnormals for e4m3 subnormals), so two exact products by powers of two
-// restore it.  A NaN code is not recognised here (it would read 480): the
-// caller looks for one with `nan_mark` and takes from_e4m3x2 instead.
-DEV uint2 dequant4(uint32_t w, __nv_bfloat162 s2) {
+// Four codes times a power of two 2^n, n <= 7, as four bf16 values, exactly: a
+// code's sign, exponent and mantissa bits moved into bf16's places read as
+// value * 2^-120 (bf16 subnormals for e4m3 subnormals), so one exact product
+// by f = 2^(120 + n) restores it.  (NaN is in the scale, never in a code.)
+DEV uint2 dequant4(uint32_t w, __nv_bfloat162 f) {
   const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
   uint32_t lo = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u);
   uint32_t hi = (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u);
-  const uint32_t k120 = 0x7b807b80u;  // 2^120 twice
-  __nv_bfloat162 x = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&lo),
-                             *reinterpret_cast<const __nv_bfloat162*>(&k120));
-  __nv_bfloat162 y = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&hi),
-                             *reinterpret_cast<const __nv_bfloat162*>(&k120));
-  x = __hmul2(x, s2);
-  y = __hmul2(y, s2);
-  return make_uint2(*reinterpret_cast<uint32_t*>(&x), *reinterpret_cast<uint32_t*>(&y));
+  const __nv_bfloat162 x = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&lo), f);
+  const __nv_bfloat162 y = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&hi), f);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
-// bits 7, 15, 23, 31 set where a code of w is NaN (0x7f or 0xff)
-DEV uint32_t nan_mark(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
-// sixteen codes times `scale` as sixteen bf16 values
-DEV void dequant16(const uint4& c, float scale, uint4& o0, uint4& o1) {
+// whether a scale of the warp is past dequant4's range
+template <int N>
+DEV bool any_big(const float (&sc)[N]) {
+  float m = sc[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = fmaxf(m, sc[i]);
+  return __any_sync(0xffffffffu, m > 128.f);
+}
+
+// sixteen codes times `scale` as sixteen bf16 values (big: the scale may be
+// above 2^7)
+DEV void dequant16(const uint4& c, float scale, bool big, uint4& o0, uint4& o1) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
   uint32_t r[8];
-  if (nan_mark(c.x) | nan_mark(c.y) | nan_mark(c.z) | nan_mark(c.w)) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 f = from_e4m3x2(w[i >> 1] >> (16 * (i & 1)));
-      r[i] = pack_bf16x2(f.x * scale, f.y * scale);
+  if (big) {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t wi = i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : w[3];
+      const float2 f = from_e4m3x2(wi), g = from_e4m3x2(wi >> 16);
+      const uint32_t a = pack_bf16x2(f.x * scale, f.y * scale);
+      const uint32_t b = pack_bf16x2(g.x * scale, g.y * scale);
+      if (i == 0) { r[0] = a; r[1] = b; }
+      if (i == 1) { r[2] = a; r[3] = b; }
+      if (i == 2) { r[4] = a; r[5] = b; }
+      if (i == 3) { r[6] = a; r[7] = b; }
     }
   } else {
-    const __nv_bfloat162 s2 = __float2bfloat162_rn(scale);
+    const __nv_bfloat162 f = __float2bfloat162_rn(scale * __uint_as_float(0x7b800000u));  // 2^120
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint2 v = dequant4(w[i], s2);
+      const uint2 v = dequant4(w[i], f);
       r[2 * i] = v.x;
       r[2 * i + 1] = v.y;
     }

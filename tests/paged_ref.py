@@ -14,18 +14,19 @@ E4M3 = torch.tensor([(c & 7) * 2.0 ** -9 if c < 8 else (1 + (c & 7) / 8) * 2.0 *
 
 def scales(lat):
     """[N, 512] -> scale of each group of 128: the least 2^n, n in [-117, 119],
-    with max |finite x| <= 448 * 2^n."""
+    with max |x| <= 448 * 2^n; NaN for a group with a NaN or an infinity."""
     x = lat.double().reshape(-1, 4, 128)
-    top = torch.where(torch.isfinite(x), x.abs(), 0.0).amax(-1)
+    top = x.abs().amax(-1)
     n = torch.full_like(top, -117.0)
     for k in range(-117, 119):
         n += (top > 448.0 * 2.0 ** k).double()
-    return torch.pow(2.0, n.cpu()).to(lat.device)
+    s = torch.pow(2.0, n.cpu()).to(lat.device)
+    return torch.where(torch.isfinite(x).all(-1), s, torch.nan)
 
 
 def codes(lat, scale):
     """Nearest e4m3 code of each value over its group's scale, ties to the even
-    code, by search in the table; NaN and infinities to code 127."""
+    code, by search in the table; 0 where the scale is NaN."""
     table = E4M3.to(lat.device)
     y = (lat.double().reshape(-1, 4, 128) / scale[..., None]).reshape(lat.shape[0], -1)
     fin = torch.isfinite(y)
@@ -34,7 +35,7 @@ def codes(lat, scale):
     lo = (hi - 1).clamp(min=0)
     dl, dh = a - table[lo], table[hi] - a
     pick = torch.where((dl < dh) | ((dl == dh) & (lo % 2 == 0)), lo, hi)
-    c = torch.where(fin, pick, 127) | torch.where(torch.signbit(y) & fin, 128, 0)
+    c = torch.where(fin, pick | torch.where(torch.signbit(y), 128, 0), 0)
     return c.to(torch.uint8)
 
 

@@ -306,7 +306,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::thread
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.p_full[i][0], 8);  // the four warps of a group in each CTA
       mbar_init(&bars.p_full[i][1], 4);  // the two of the second half
-      mbar_init(&bars.v_full[i], fill);
+      mbar_init(&bars.v_full[i], kE4M3 ? Roles<true>::load_warps : 1);
       mbar_init(&bars.pv_done[i][0], 1);
       mbar_init(&bars.pv_done[i][1], 1);
       mbar_init(&bars.x_full[i][0], 2);
@@ -356,9 +356,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::thread
         enter();
       }
     };
-    // an entry outside the pool counts once for each page of a sequence
-    auto row_at = [&](int pg, int off, bool count) {
+    // the pool row of position k, whose page is pg; an entry outside the pool
+    // counts once for each page of a sequence
+    auto row_at = [&](int pg, int k, bool count) {
       const bool in = pg >= 0 && pg < p.pool.num_pages;
+      const int off = k - page_of(p.pool, k) * p.pool.page_size;
       if (count && !in && off == 0) ++bad;
       return in ? pg * p.pool.pitch + off : p.pool.rows;
     };
@@ -379,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::thread
         auto lookup = [&]() {
           advance();
           const int k = jt * KT + sub;
-          if (p.box == 64 && k + 64 <= lim) pg = ld_global_nc_s32_early(trow + k / p.pool.page_size);
+          if (p.box == 64 && k + 64 <= lim) pg = ld_global_nc_s32_early(trow + page_of(p.pool, k));
         };
         lookup();
 #pragma unroll 1
@@ -388,11 +390,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::thread
           const bool whole = p.box == 64 && left >= 64;
           int y0 = 0, r0 = p.pool.rows, r1 = p.pool.rows;  // rows of keys k0, k0 + lane, k0 + 32 + lane
           if (whole) {
-            y0 = row_at(pg, k0 % p.pool.page_size, counts && last && lane == 0);
+            y0 = row_at(pg, k0, counts && last && lane == 0);
           } else {
-            const int ka = k0 + lane, kb = ka + 32, ps = p.pool.page_size;
-            if (ka < lim) r0 = row_at(ld_global_nc_s32_early(trow + ka / ps), ka % ps, counts && last);
-            if (kb < lim) r1 = row_at(ld_global_nc_s32_early(trow + kb / ps), kb % ps, counts && last);
+            const int ka = k0 + lane, kb = ka + 32;
+            if (ka < lim)
+              r0 = row_at(ld_global_nc_s32_early(trow + page_of(p.pool, ka)), ka, counts && last);
+            if (kb < lim)
+              r1 = row_at(ld_global_nc_s32_early(trow + page_of(p.pool, kb)), kb, counts && last);
           }
           if (i + 1 < n) lookup();
           const bool ok =
@@ -432,112 +436,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::thread
         }
       }
     } else {
-      // 8-bit: a tile in two steps of 1024 units of 16 codes, four a thread.  Keys:
-      // 32 rows of 32 units a step (and one 16-byte piece of a rotary key a
-      // thread); values: 64 rows (half of the keys) of 16 units.  The next step's
-      // loads are in flight while this one's codes are converted: 36 KB an SM.
-      // Groups of 32 keys: two a tile for keys (this CTA's 64), four for values.
-      // Lane l looks up the page of each group's l-th key, a tile ahead: r[g] is
-      // its pool row for the current tile, pg[g] its page for the next.
-      const int groups = val ? 4 : 2, sub = val ? 0 : rank * 64;
-      int r[4], pg[4];
-      auto fetch = [&]() {  // the next tile's pages
+      // 8-bit: two neighbouring threads take 256 codes of a row, 16 of every 32
+      // bytes each, with their two scales (and, for keys, a quarter of its rotary
+      // key): 256 threads for the 64 rows x 512 codes of the keys, as many for
+      // the 128 x 256 of the values.  A tile is converted as soon as its place is
+      // free; then the next one's loads are issued, 64 KB an SM in flight.  (With
+      // the row's codes across the lanes of a warp, in steps, address work and
+      // loads stood between a free place and its next tile: 9000 cycles a tile.)
+      const int t = wl * 32 + lane, b = t & 1;
+      const int row = val ? t >> 1 : t >> 2, h = val ? rank : (t >> 1) & 1;
+      const int key = row + (val ? 0 : rank * 64);  // of the tile
+      const int hf = val ? wl >> 2 : 0;             // half of the values' keys
+      uint64_t* const full = val ? &bars.v_full[hf] : &bars.k_full[0];
+      const uint32_t full0 = first_cta(full);
+      // 16-byte piece 2b of an atom's row (pieces + 1, + 4, + 5: address ^ 16, 64, 80)
+      const uint32_t d0 = sbase + (val ? OFF_V + hf * V_CHUNK : OFF_K + h * 4 * K_ATOM) +
+                          sw128_off(row & 63, 2 * b);
+      const uint32_t d1 = d0 ^ 16u, d2 = d0 ^ 64u, d3 = d0 ^ 80u;
+      const uint32_t r0 = sbase + OFF_K + 8 * K_ATOM + sw128_off(row & 63, 4 * h + 2 * b);
+      uint4 code[8];
+      const uint8_t* rope = nullptr;  // this thread's 32 bytes of the rotary key
+      float2 sc;
+      bool in = false;
+      int pg = -2;  // page of this thread's key in the next tile to load
+      auto lookup = [&]() {
         advance();
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int k = jt * KT + sub + g * 32 + lane;
-          pg[g] = -2;
-          if (g < groups && k < lim) pg[g] = ld_global_nc_s32_early(trow + k / p.pool.page_size);
-        }
+        const int k = jt * KT + key;
+        pg = -2;
+        if (k < lim) pg = ld_global_nc_s32_early(trow + page_of(p.pool, k));
       };
-      auto enter_tile = [&](bool more) {  // the fetched tile becomes the current one
+      auto load = [&]() {
+        const int k = jt * KT + key;
+        int y = row_at(pg, k, val && rank == 0 && b == 0 && last && k < lim);
+        in = y < p.pool.rows;
+        if (!in) y = 0;  // (any row: its values are multiplied by 0)
+        const uint8_t* src = p.pool.base + (long long)y * p.pool.row_stride;
+        const uint8_t* c = src + h * 256 + b * 16;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          if (g >= groups) break;
-          const int k = jt * KT + sub + g * 32 + lane;
-          r[g] = row_at(pg[g], k % p.pool.page_size,
-                        val && rank == 0 && wl == 0 && last && k < lim);
-        }
-        if (more) fetch();
+        for (int j = 0; j < 8; ++j) code[j] = ld_global_nc_v4(c + j * 32);
+        sc = *reinterpret_cast<const float2*>(src + pages::kScaleOff + h * 8);
+        rope = src + pages::kRopeOff + (2 * h + b) * 32;
       };
-      fetch();
-      uint4 code[4], rope = make_uint4(0, 0, 0, 0);
-      float sc[4];
-      const int ch = val ? lane & 15 : lane;                    // unit of a row
-      const int soff = pages::kScaleOff + (val ? rank * 2 + (ch >> 3) : lane >> 3) * 4;
-      const int uoff = val ? rank * 256 + ch * 16 : lane * 16;
-      // row of this thread's unit `it` in the step
-      const int row0 = val ? wl * 8 + (lane >> 4) : wl * 4, row_it = val ? 2 : 1;
-      auto load = [&](int st) {
-        // (a warp's rows lie in one group)
-        const int rows = !val ? (st ? r[1] : r[0])
-                         : wl < 4 ? (st ? r[2] : r[0]) : (st ? r[3] : r[1]);
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          const int y = __shfl_sync(0xffffffffu, rows, (row0 + it * row_it) & 31);
-          code[it] = make_uint4(0, 0, 0, 0);
-          sc[it] = 1.f;
-          if (y < p.pool.rows) {
-            const uint8_t* src = p.pool.base + (long long)y * p.pool.row_stride;
-            code[it] = ld_global_nc_v4(src + uoff);
-            sc[it] = u2f((uint32_t)ld_global_nc_s32_early(reinterpret_cast<const int32_t*>(src + soff)));
-          }
-        }
-        if (!val) {
-          const int y = __shfl_sync(0xffffffffu, rows, wl * 4 + (lane >> 3));
-          rope = make_uint4(0, 0, 0, 0);
-          if (y < p.pool.rows)
-            rope = ld_global_nc_v4(p.pool.base + (long long)y * p.pool.row_stride +
-                                   pages::kRopeOff + (lane & 7) * 16);
-        }
-      };
-      const uint32_t full0 = first_cta(val ? &bars.v_full[0] : &bars.k_full[0]);
-      const uint32_t atom0 =
-          val ? sbase + OFF_V + (ch >> 2) * V_ATOM : sbase + OFF_K + (lane >> 2) * K_ATOM;
-      const int c2 = (ch & 3) * 2;
-      bool ok = true;
-      enter_tile(n > 1);
-      load(0);
+      lookup();
+      load();
+      if (n > 1) lookup();
 #pragma unroll 1
-      for (int q = 0; q < 2 * n; ++q) {
-        const int i = q >> 1, st = q & 1;
-        if (val) {
-          if (i > 0)
-            ok = warp_wait(&bars.pv_done[(i - 1) & 1][st], ((i - 1) >> 1) & 1, abort, p.status);
-        } else if (st == 0) {
-          // (the last chunk's products are the last to finish)
-          ok = warp_wait(&bars.k_empty[NKC - 1], (i & 1) ^ 1, abort, p.status);
-        }
+      for (int i = 0; i < n; ++i) {
+        // (keys: the last chunk's products are the last to finish)
+        const bool ok =
+            val ? i == 0 || warp_wait(&bars.pv_done[(i - 1) & 1][hf], ((i - 1) >> 1) & 1, abort,
+                                      p.status)
+                : warp_wait(&bars.k_empty[NKC - 1], (i & 1) ^ 1, abort, p.status);
         if (!ok) break;
-        const uint32_t atom = atom0 + (val ? st * V_CHUNK : 0);
-        const int rbase = row0 + (val ? 0 : st * 32);
-        const bool big = pages::any_big(sc);
+        if (!val) {  // (no registers for these: they arrive during the conversion)
+          cp_async_16(r0, rope, in ? 16u : 0u);
+          cp_async_16(r0 ^ 16u, rope + 16, in ? 16u : 0u);
+        }
+        if (!in) sc = make_float2(0.f, 0.f);
+        const pages::Factor f0(sc.x), f1(sc.y);
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          const int row = rbase + it * row_it;
+        for (int j = 0; j < 8; ++j) {
           uint4 o0, o1;
-          pages::dequant16(code[it], sc[it], big, o0, o1);
-          st_shared_v4(atom + sw128_off(row, c2), o0.x, o0.y, o0.z, o0.w);
-          st_shared_v4(atom + sw128_off(row, c2 + 1), o1.x, o1.y, o1.z, o1.w);
+          pages::dequant16(code[j], j < 4 ? f0 : f1, o0, o1);
+          st_shared_v4((j & 1 ? d2 : d0) + (j >> 1) * 8192, o0.x, o0.y, o0.z, o0.w);
+          st_shared_v4((j & 1 ? d3 : d1) + (j >> 1) * 8192, o1.x, o1.y, o1.z, o1.w);
         }
-        if (!val)
-          st_shared_v4(sbase + OFF_K + 8 * K_ATOM +
-                           sw128_off(st * 32 + wl * 4 + (lane >> 3), lane & 7),
-                       rope.x, rope.y, rope.z, rope.w);
-        if (q + 1 < 2 * n) {
-          if (st == 1) enter_tile(i + 2 < n);
-          load(st ^ 1);
+        cp_async_wait_all();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_pair(full0);
+          if (!val)
+            for (int k = 1; k < NKC; ++k) mbar_arrive_pair(full0 + k * 8);
         }
-        if (val || st == 1) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (val) {
-              mbar_arrive_pair(full0 + st * 8);
-            } else {
-              for (int k = 0; k < NKC; ++k) mbar_arrive_pair(full0 + k * 8);
-            }
-          }
+        if (i + 1 < n) {
+          load();
+          if (i + 2 < n) lookup();
         }
       }
     }
@@ -1303,6 +1277,7 @@ extern "C" int mla_attend_paged(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe
   p.row_stride = row_stride;
   p.rows = (num_pages - 1) * p.pitch + page_size;
   p.table = page_table;
+  paged::set_division(&p);
   p.max_pages = max_pages;
   paged::Seqs q;
   q.cu_q = cu_q;

@@ -23,9 +23,24 @@ struct Pool {
   int pitch;              // rows from one page to the next
   int row_stride;         // bytes
   int rows;               // rows from the first page's first to the last page's last
+  uint32_t magic;         // pos / page_size = pos * magic >> shift, for 0 <= pos <= 2^24
+  int shift;
   const int32_t* table;   // [S][max_pages]
   int max_pages;
 };
+
+// With 2^b >= page_size, shift = 24 + b and magic = ceil(2^shift / page_size), the
+// product overshoots pos * 2^shift / page_size by less than pos <= 2^24 <=
+// 2^shift / page_size: not as far as the next whole quotient.
+inline void set_division(Pool* p) {
+  int b = 0;
+  while ((1ll << b) < p->page_size) ++b;
+  p->shift = 24 + b;
+  p->magic = (uint32_t)(((1ull << p->shift) + p->page_size - 1) / p->page_size);
+}
+DEV int page_of(const Pool& p, int pos) {
+  return (int)((uint64_t)(uint32_t)pos * p.magic >> p.shift);
+}
 
 // The sequences of a call: sequence s has new tokens cu_q[s] .. cu_q[s+1]-1
 // and kv_len[s] cached positions, the new tokens' own among them.
@@ -46,7 +61,7 @@ struct Seqs {
 // The row of position `pos` of the sequence whose table row is `t`, or
 // `p.rows` (past the end: reads as zeros) when the table holds no valid page.
 DEV int row_of(const Pool& p, const int32_t* t, int pos) {
-  const int pg = pos / p.page_size;
+  const int pg = page_of(p, pos);
   const int page = ld_global_nc_s32_early(t + pg);
   return page >= 0 && page < p.num_pages ? page * p.pitch + (pos - pg * p.page_size) : p.rows;
 }

@@ -77,43 +77,33 @@ DEV uint2 dequant4(uint32_t w, __nv_bfloat162 f) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
-// whether a scale of the warp is past dequant4's range
-template <int N>
-DEV bool any_big(const float (&sc)[N]) {
-  float m = sc[0];
-#pragma unroll
-  for (int i = 1; i < N; ++i) m = fmaxf(m, sc[i]);
-  return __any_sync(0xffffffffu, m > 128.f);
+// The same for any scale: through fp32.  Out of line, for scales above 2^7.
+static __device__ __noinline__ uint4 dequant8_any(uint2 c, float scale) {
+  const float2 a = from_e4m3x2(c.x), b = from_e4m3x2(c.x >> 16);
+  const float2 d = from_e4m3x2(c.y), e = from_e4m3x2(c.y >> 16);
+  return make_uint4(pack_bf16x2(a.x * scale, a.y * scale), pack_bf16x2(b.x * scale, b.y * scale),
+                    pack_bf16x2(d.x * scale, d.y * scale), pack_bf16x2(e.x * scale, e.y * scale));
 }
 
-// sixteen codes times `scale` as sixteen bf16 values (big: the scale may be
-// above 2^7)
-DEV void dequant16(const uint4& c, float scale, bool big, uint4& o0, uint4& o1) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  uint32_t r[8];
-  if (big) {
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t wi = i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : w[3];
-      const float2 f = from_e4m3x2(wi), g = from_e4m3x2(wi >> 16);
-      const uint32_t a = pack_bf16x2(f.x * scale, f.y * scale);
-      const uint32_t b = pack_bf16x2(g.x * scale, g.y * scale);
-      if (i == 0) { r[0] = a; r[1] = b; }
-      if (i == 1) { r[2] = a; r[3] = b; }
-      if (i == 2) { r[4] = a; r[5] = b; }
-      if (i == 3) { r[6] = a; r[7] = b; }
-    }
-  } else {
-    const __nv_bfloat162 f = __float2bfloat162_rn(scale * __uint_as_float(0x7b800000u));  // 2^120
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint2 v = dequant4(w[i], f);
-      r[2 * i] = v.x;
-      r[2 * i + 1] = v.y;
-    }
+// a scale and what dequant4 multiplies by
+struct Factor {
+  float scale;
+  __nv_bfloat162 f;
+  DEV explicit Factor(float s)
+      : scale(s), f(__float2bfloat162_rn(s * 1.329227995784916e36f)) {}  // 2^120
+};
+
+// sixteen codes times a scale as sixteen bf16 values
+DEV void dequant16(const uint4& c, const Factor& f, uint4& o0, uint4& o1) {
+  if (f.scale > 128.f) {
+    o0 = dequant8_any(make_uint2(c.x, c.y), f.scale);
+    o1 = dequant8_any(make_uint2(c.z, c.w), f.scale);
+    return;
   }
-  o0 = make_uint4(r[0], r[1], r[2], r[3]);
-  o1 = make_uint4(r[4], r[5], r[6], r[7]);
+  const uint2 a = dequant4(c.x, f.f), b = dequant4(c.y, f.f), d = dequant4(c.z, f.f),
+              e = dequant4(c.w, f.f);
+  o0 = make_uint4(a.x, a.y, b.x, b.y);
+  o1 = make_uint4(d.x, d.y, e.x, e.y);
 }
 
 }  // namespace pages

@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Seqs q, const Pool poo
 //                warp for all chunks took 700 cycles for each, in turn).  8-bit:
 //                loads, exact conversion to bf16 and swizzled stores.
 //   then one warp each that issues the score products (first CTA; TMEM owner),
-//                loads queries (TMA), and issues the value products (first CTA)
+//                loads queries (TMA), issues the value products (first CTA) and
+//                loads the rotary keys of 8-bit pages (TMA)
 // TMEM (512 columns): four score tiles [0,256), output [256,512).
 // ===========================================================================
 
@@ -197,7 +198,7 @@ constexpr int KEY_WARP0 = 8;
 template <bool kE4M3>
 struct Roles {
   static constexpr int load_warps = kE4M3 ? 8 : 4;  // of keys, and of values
-  static constexpr int val0 = KEY_WARP0 + load_warps, s = val0 + load_warps, q = s + 1, o = s + 2;
+  static constexpr int val0 = KEY_WARP0 + load_warps, s = val0 + load_warps, q = s + 1, o = s + 2, rope = s + 3;
   static constexpr int threads = 32 * (s + 4);
   // registers: an equal share at launch, then by role (in groups of four warps)
   static constexpr int groups = threads / 128, share = 65536 / threads / 8 * 8;
@@ -297,10 +298,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::thread
   if (warp == R::s) tmem_alloc2(&bars.tmem_base, TMEM_COLS);
   if (tid == 0) {
     constexpr int fill = kE4M3 ? 2 * Roles<true>::load_warps : 1;  // warps of both CTAs, or one arrival and bytes
+    constexpr int rope_fill = kE4M3 ? 1 : 0;  // (the last chunk also a box of rotary keys)
     mbar_init(&bars.q_full, 1);
     mbar_init(&bars.q_free, 1);
     for (int i = 0; i < NKC; ++i) {
-      mbar_init(&bars.k_full[i], fill);
+      mbar_init(&bars.k_full[i], fill + (i == NKC - 1 ? rope_fill : 0));
       mbar_init(&bars.k_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -436,46 +438,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::thread
         }
       }
     } else {
-      // 8-bit: two neighbouring threads take 256 codes of a row, 16 of every 32
-      // bytes each, with their two scales (and, for keys, a quarter of its rotary
-      // key): 256 threads for the 64 rows x 512 codes of the keys, as many for
-      // the 128 x 256 of the values.  A tile is converted as soon as its place is
-      // free; then the next one's loads are issued, 64 KB an SM in flight.  (With
-      // the row's codes across the lanes of a warp, in steps, address work and
-      // loads stood between a free place and its next tile: 9000 cycles a tile.)
-      const int t = wl * 32 + lane, b = t & 1;
-      const int row = val ? t >> 1 : t >> 2, h = val ? rank : (t >> 1) & 1;
-      const int key = row + (val ? 0 : rank * 64);  // of the tile
-      const int hf = val ? wl >> 2 : 0;             // half of the values' keys
+      // 8-bit: a warp takes 8 rows x 512 codes of the keys, or 16 x 256 of the
+      // values: eight loads of 16 codes a thread, each instruction two rows' 256
+      // contiguous bytes (four cache lines; a thread's codes side by side would
+      // be 16 lines an instruction), and one scale, passed on by shuffles.  A
+      // tile is converted as soon as its place is free; then the next one's loads
+      // are issued, 64 KB an SM in flight.  The rotary keys come by TMA.
+      const int hi = lane >> 4, ch = lane & 15;        // row of an instruction's pair, unit
+      const int rows = val ? 16 : 8, hf = val ? wl >> 2 : 0;
+      const int row0 = wl * rows;                      // of the tile's (this CTA's) rows
+      const int yl = lane & (rows - 1);                // the row whose page this lane looks up
+      const int key = row0 + yl + (val ? 0 : rank * 64);
       uint64_t* const full = val ? &bars.v_full[hf] : &bars.k_full[0];
       const uint32_t full0 = first_cta(full);
-      // 16-byte piece 2b of an atom's row (pieces + 1, + 4, + 5: address ^ 16, 64, 80)
-      const uint32_t d0 = sbase + (val ? OFF_V + hf * V_CHUNK : OFF_K + h * 4 * K_ATOM) +
-                          sw128_off(row & 63, 2 * b);
-      const uint32_t d1 = d0 ^ 16u, d2 = d0 ^ 64u, d3 = d0 ^ 80u;
-      const uint32_t r0 = sbase + OFF_K + 8 * K_ATOM + sw128_off(row & 63, 4 * h + 2 * b);
+      // 16-byte piece of the first pair's row: pair j's is at (d0 ^ (j << 5)) + 256 j
+      // (j < 4), the piece after it at address ^ 16
+      const uint32_t d0 = sbase + (val ? OFF_V + hf * V_CHUNK : OFF_K) + (ch >> 2) * K_ATOM +
+                          sw128_off((row0 & 63) + hi, (ch & 3) * 2);
+      const int coff = (val ? rank * 256 : 0) + ch * 16;
+      const int srow = val ? lane >> 1 : lane >> 2;    // row and group of this lane's scale
+      const int soff = pages::kScaleOff + (val ? rank * 2 + (lane & 1) : lane & 3) * 4;
+      // lane that holds the scale of unit it
+      const int s0 = val ? hi * 2 + (ch >> 3) : hi * 4 + (ch >> 3);
       uint4 code[8];
-      const uint8_t* rope = nullptr;  // this thread's 32 bytes of the rotary key
-      float2 sc;
-      bool in = false;
-      int pg = -2;  // page of this thread's key in the next tile to load
+      float sc = 0.f;
+      int y = 0, pg = -2;  // pool row of the tile loaded, page of the next (this lane's row)
       auto lookup = [&]() {
         advance();
         const int k = jt * KT + key;
         pg = -2;
         if (k < lim) pg = ld_global_nc_s32_early(trow + page_of(p.pool, k));
       };
+      auto ptr = [&](int l) {  // the row of lane l (an absent one: any, it gets the factor 0)
+        const int r = __shfl_sync(0xffffffffu, y, l);
+        return p.pool.base + (long long)(r < p.pool.rows ? r : 0) * p.pool.row_stride;
+      };
       auto load = [&]() {
         const int k = jt * KT + key;
-        int y = row_at(pg, k, val && rank == 0 && b == 0 && last && k < lim);
-        in = y < p.pool.rows;
-        if (!in) y = 0;  // (any row: its values are multiplied by 0)
-        const uint8_t* src = p.pool.base + (long long)y * p.pool.row_stride;
-        const uint8_t* c = src + h * 256 + b * 16;
+        y = row_at(pg, k, val && rank == 0 && lane < rows && last && k < lim);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) code[j] = ld_global_nc_v4(c + j * 32);
-        sc = *reinterpret_cast<const float2*>(src + pages::kScaleOff + h * 8);
-        rope = src + pages::kRopeOff + (2 * h + b) * 32;
+        for (int it = 0; it < 8; ++it)
+          code[it] = ld_global_nc_v4(val ? ptr(it * 2 + hi) + coff
+                                         : ptr((it >> 1) * 2 + hi) + coff + (it & 1) * 256);
+        const uint8_t* src = ptr(srow);
+        sc = *reinterpret_cast<const float*>(src + soff);
       };
       lookup();
       load();
@@ -488,20 +494,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::thread
                                       p.status)
                 : warp_wait(&bars.k_empty[NKC - 1], (i & 1) ^ 1, abort, p.status);
         if (!ok) break;
-        if (!val) {  // (no registers for these: they arrive during the conversion)
-          cp_async_16(r0, rope, in ? 16u : 0u);
-          cp_async_16(r0 ^ 16u, rope + 16, in ? 16u : 0u);
-        }
-        if (!in) sc = make_float2(0.f, 0.f);
-        const pages::Factor f0(sc.x), f1(sc.y);
+        if (__shfl_sync(0xffffffffu, y, srow) >= p.pool.rows) sc = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int it = 0; it < 8; ++it) {
+          const int j = val ? it & 3 : it >> 1;  // pair of rows (mod 8 rows)
+          const uint32_t off = j * 256 + (val ? (it >> 2) * 1024 : (it & 1) * 4 * K_ATOM);
+          const float f = __shfl_sync(0xffffffffu, sc, s0 + (val ? it * 4 : j * 8 + (it & 1) * 2));
           uint4 o0, o1;
-          pages::dequant16(code[j], j < 4 ? f0 : f1, o0, o1);
-          st_shared_v4((j & 1 ? d2 : d0) + (j >> 1) * 8192, o0.x, o0.y, o0.z, o0.w);
-          st_shared_v4((j & 1 ? d3 : d1) + (j >> 1) * 8192, o1.x, o1.y, o1.z, o1.w);
+          pages::dequant16(code[it], pages::Factor(f), o0, o1);
+          st_shared_v4((d0 ^ (j << 5)) + off, o0.x, o0.y, o0.z, o0.w);
+          st_shared_v4((d0 ^ (j << 5) ^ 16u) + off, o1.x, o1.y, o1.z, o1.w);
         }
-        cp_async_wait_all();
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -517,6 +520,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::thread
     }
     bad = __reduce_add_sync(0xffffffffu, bad);
     if (lane == 0 && bad && p.status) atomicAdd(p.status + 1, bad);
+  } else if (kE4M3 && warp == R::rope) {
+    // ---------------- rotary keys of 8-bit pages: the last atom of the last chunk ----------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::rest));
+    int bb = bb0, jt = jt0 - 1, nr = tiles_of(bb0), lim = 0;
+    const int32_t* trow = nullptr;
+    auto enter = [&]() {
+      if (bb >= p.N) return;
+      lim = lim_of(bb);
+      trow = p.pool.table + (long long)ld_global_nc_s32_early(p.plan.seq + bb) * p.pool.max_pages;
+    };
+    enter();
+    const uint32_t bar = first_cta(&bars.k_full[NKC - 1]), dst = sbase + OFF_K + 8 * K_ATOM;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      if (++jt == nr) {
+        jt = 0;
+        nr = tiles_of(++bb);
+        enter();
+      }
+      const int k0 = jt * KT + rank * 64 + lane, first = k0 - lane;
+      const int r0 = k0 < lim ? row_of(p.pool, trow, k0) : p.pool.rows;
+      const int r1 = k0 + 32 < lim ? row_of(p.pool, trow, k0 + 32) : p.pool.rows;
+      if (!warp_wait(&bars.k_empty[NKC - 1], (i & 1) ^ 1, abort, p.status)) break;
+      if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&bars.k_full[NKC - 1], 2 * K_ATOM);
+      __syncwarp();
+      if (p.box && first + 64 <= lim) {
+        const int k = lane * p.box & 63;
+        const int ya = __shfl_sync(0xffffffffu, r0, k & 31);
+        const int yb = __shfl_sync(0xffffffffu, r1, k & 31);
+        if (lane * p.box < 64) tma_load_2d_pair(dst + k * 128, &map_b, 0, k < 32 ? ya : yb, bar);
+      } else {
+        const int g = lane & 15;
+        int y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int ya = __shfl_sync(0xffffffffu, r0, (4 * g + j) & 31);
+          const int yb = __shfl_sync(0xffffffffu, r1, (4 * g + j) & 31);
+          y[j] = g < 8 ? ya : yb;
+        }
+        if (lane < 16) tma_gather4_pair(dst + g * 512, &map_1, 0, y[0], y[1], y[2], y[3], bar);
+      }
+      __syncwarp();
+    }
   } else if (warp == R::q) {
     // ---------------- queries: this CTA's 64 heads of each token ----------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::rest));
@@ -1169,6 +1215,11 @@ static int launch_absorbed(const Params& p, int nc, cudaStream_t st) {
     if (int e = bf16_map_3d(&map_v, p.pool.base, 64, rows, 9, rb, 128, 64, 64, 4)) return e;
     if (int e = bf16_map_2d(&map_b, p.pool.base, MLA_ROW, rows, rb, 64, p.box ? p.box : 1)) return e;
     if (int e = bf16_map_2d(&map_1, p.pool.base, MLA_ROW, rows, rb, 64, 1)) return e;
+  } else {
+    const uint64_t rows = p.pool.rows, rb = p.pool.row_stride;
+    const uint8_t* rope = p.pool.base + pages::kRopeOff;
+    if (int e = bf16_map_2d(&map_b, rope, kR, rows, rb, 64, p.box ? p.box : 1)) return e;
+    if (int e = bf16_map_2d(&map_1, rope, kR, rows, rb, 64, 1)) return e;
   }
   static std::atomic<unsigned long long> attr_done{0};
   if (int e = ensure_smem_attr(absorbed_kernel<kE4M3>, dynamic_smem(), &attr_done)) return e;

@@ -448,8 +448,8 @@ int mla_page_read(const void* pool, int kind, int num_pages, int page_size, int6
  *              (81,920 flop per token and position).  MLA_FORM_AUTO takes the
  *              expanded form from an average of 128 new tokens a sequence on.
  *              The forms agree within rounding.
- *   ws         at least mla_attend_paged_workspace_bytes(N, S, max_kv, form)
- *              bytes, 256-byte aligned; contents need not be initialised
+ *   ws         at least mla_attend_paged_workspace_bytes(N, S, max_kv, kind,
+ *              form) bytes, 256-byte aligned; contents need not be initialised
  *   status     optional int32[2].  An entry of page_table outside [0, num_pages)
  *              for a page below a sequence's length reads as a page of zeros
  *              and is counted once in status[1].
@@ -462,6 +462,9 @@ int mla_page_read(const void* pool, int kind, int num_pages, int page_size, int6
  * 128, at most 2^26 (else MLA_ERR_SHAPE).  The expanded form's workspace holds
  * 1152 bytes for each of those positions and the keys and values of as many
  * heads as fit 4 GiB, at least 8 (4 KB a position) and at most 128 (64 KB).
+ * The absorbed form on 8-bit pages with three tokens a sequence or more on
+ * average (N >= 3 S, N * max_kv >= 2^18) converts the positions to bf16 in the
+ * workspace first, 1152 bytes each, where that is 4 GiB at most.
  *
  * Arithmetic: scores, softmax statistics and outputs accumulate in fp32.
  * Rounded to bf16, as tensor-core operands: softmax weights; absorbed: q~, the
@@ -473,7 +476,7 @@ int mla_page_read(const void* pool, int kind, int num_pages, int page_size, int6
  * semantics for the caller).  The call can be captured into a graph; graphs
  * that may run at the same time need workspaces of their own.
  */
-size_t mla_attend_paged_workspace_bytes(int N, int S, int max_kv, int form);
+size_t mla_attend_paged_workspace_bytes(int N, int S, int max_kv, int kind, int form);
 int mla_attend_paged(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const mla_bf16_t* wkv_b,
                      const void* pool, int kind, int num_pages, int page_size,
                      int64_t page_stride, int row_stride, const int32_t* page_table,

@@ -51,7 +51,7 @@ _SIGS = {
                                 _c_int, _vp, _vp]),
     "mla_page_read": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_i64, _c_int, _vp, _c_int, _vp,
                                _c_i64, _vp, _vp]),
-    "mla_attend_paged_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int]),
+    "mla_attend_paged_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int]),
     "mla_attend_paged": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_i64, _c_int,
                                   _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_float,
                                   _c_int, _vp, _vp, _c_size, _vp, _vp]),
@@ -437,10 +437,14 @@ def mla_page_read(pages: torch.Tensor, slots: torch.Tensor, out: Optional[torch.
     return out
 
 
-def mla_attend_paged_workspace_bytes(N: int, S: int, max_kv: int, form: str = "auto") -> int:
-    if form not in FORMS:
-        raise MLAError(f"form must be one of {', '.join(FORMS)}")
-    return int(LIB.mla_attend_paged_workspace_bytes(int(N), int(S), int(max_kv), FORMS[form]))
+def mla_attend_paged_workspace_bytes(N: int, S: int, max_kv: int, bits: int,
+                                     form: str = "auto") -> int:
+    """Bytes for N tokens of S sequences of at most max_kv positions in 8- or
+    16-bit pages."""
+    if form not in FORMS or bits not in (8, 16):
+        raise MLAError(f"form must be one of {', '.join(FORMS)}, bits 8 or 16")
+    return int(LIB.mla_attend_paged_workspace_bytes(int(N), int(S), int(max_kv), int(bits == 8),
+                                                    FORMS[form]))
 
 
 def mla_attend_paged(q_nope: torch.Tensor, q_pe: torch.Tensor, wkv_b: torch.Tensor,
@@ -480,7 +484,7 @@ def mla_attend_paged(q_nope: torch.Tensor, q_pe: torch.Tensor, wkv_b: torch.Tens
     pool, kind, P, ps, page, row = _pool(pages)
     with torch.cuda.device(dev):
         if ws is None:
-            ws = torch.empty(mla_attend_paged_workspace_bytes(N, S, max_kv, form),
+            ws = torch.empty(mla_attend_paged_workspace_bytes(N, S, max_kv, 8 if kind else 16, form),
                              dtype=torch.uint8, device=dev)
         _check(LIB.mla_attend_paged(_p(q_nope), _p(q_pe), _p(wkv_b), pool, kind, P, ps, page, row,
                                     _p(page_table), page_table.shape[1], _p(cu_q), _p(kv_len), S,

@@ -1227,11 +1227,31 @@ static int launch_absorbed(const Params& p, int nc, cudaStream_t st) {
                     map_qt, map_qr, map_k, map_v, map_b, map_1);
 }
 
+// 8-bit pages that several tokens a sequence read are converted to bf16 rows
+// first.  Measured over 128 sequences up to 16000 positions, in microseconds
+// without / with it: 2 tokens each 905 / 873, 3 1421 / 1211, 4 1784 / 1413; its
+// two launches take 10 at least (32 sequences up to 500, 2 tokens: 51 / 63; one of
+// 60000, 4 tokens: 143 / 121).  So from 3 tokens a sequence, and where what is
+// saved (0.24 ns a token and position, half of max_kv on average) pays for the
+// launches; and not where the rows could pass 4 GiB.
+static bool stages(int kind, int N, int S, int max_kv) {
+  return kind == MLA_PAGE_E4M3 && N >= 3 * (int64_t)S && (int64_t)N * max_kv >= (1 << 18) &&
+         (int64_t)S * (max_kv + 127) * (MLA_ROW * 2) <= (4ll << 30);
+}
+
 static int run_absorbed(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const mla_bf16_t* wkv_b,
-                        const Pool& pool, const Seqs& q, float scale, mla_bf16_t* O, uint8_t* ws,
-                        int32_t* status, cudaStream_t st) {
+                        const Pool& pages, const Seqs& seqs, float scale, mla_bf16_t* O,
+                        uint8_t* ws, int32_t* status, cudaStream_t st) {
   const int nc = max_pairs();
-  const AbsorbedWs L = absorbed_ws(q.N, nc);
+  const AbsorbedWs L = absorbed_ws(seqs.N, nc);
+  Pool pool = pages;
+  Seqs q = seqs;
+  if (stages(pages.kind, q.N, q.S, q.max_kv)) {
+    if (int e = expand::stage(pages, q, ws + round_up(L.total, 256), status, st, &pool)) return e;
+    // (the staged table may have room for positions that the caller's has not)
+    const int64_t cap = (int64_t)pages.max_pages * pages.page_size;
+    if (cap < q.max_kv) q.max_kv = (int)cap;
+  }
   Plan pl;
   pl.seq = reinterpret_cast<int32_t*>(ws + L.seq);
   pl.lim = reinterpret_cast<int32_t*>(ws + L.lim);
@@ -1284,7 +1304,8 @@ static int form_of(int form, int N, int S) {
   return (int64_t)N >= (int64_t)S * expand::kMinTokens ? MLA_FORM_EXPANDED : MLA_FORM_ABSORBED;
 }
 
-static int check_sizes(int N, int S, int max_kv, int form) {
+static int check_sizes(int N, int S, int max_kv, int kind, int form) {
+  if (kind != MLA_PAGE_BF16 && kind != MLA_PAGE_E4M3) return MLA_ERR_SHAPE;
   if (N < 1 || N > 65535 || S < 1 || S > 65535 || max_kv < 1 || max_kv > (1 << 24))
     return MLA_ERR_SHAPE;
   if (form < MLA_FORM_AUTO || form > MLA_FORM_EXPANDED) return MLA_ERR_SHAPE;
@@ -1295,10 +1316,11 @@ static int check_sizes(int N, int S, int max_kv, int form) {
   return MLA_OK;
 }
 
-extern "C" size_t mla_attend_paged_workspace_bytes(int N, int S, int max_kv, int form) {
-  if (check_sizes(N, S, max_kv, form) != MLA_OK) return 0;
+extern "C" size_t mla_attend_paged_workspace_bytes(int N, int S, int max_kv, int kind, int form) {
+  if (check_sizes(N, S, max_kv, kind, form) != MLA_OK) return 0;
   if (form_of(form, N, S) == MLA_FORM_EXPANDED) return expand::workspace_bytes(N, S, max_kv);
-  return paged::absorbed_ws(N, paged::max_pairs()).total;
+  const size_t own = round_up(paged::absorbed_ws(N, paged::max_pairs()).total, 256);
+  return own + (paged::stages(kind, N, S, max_kv) ? expand::staged_bytes(N, S, max_kv) : 0);
 }
 
 extern "C" int mla_attend_paged(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe,
@@ -1311,14 +1333,15 @@ extern "C" int mla_attend_paged(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe
   if (!q_nope || !q_pe || !wkv_b || !page_table || !cu_q || !kv_len || !O) return MLA_ERR_NULL;
   if (int e = pages::check_pool(pool, kind, num_pages, page_size, page_stride, row_stride))
     return e;
-  if (int e = check_sizes(N, S, max_kv, form)) return e;
+  if (int e = check_sizes(N, S, max_kv, kind, form)) return e;
   // (written so that a NaN is refused too)
   if (max_pages < 1 || !(scale > 0.f && scale <= 3.0e38f)) return MLA_ERR_SHAPE;
   if (!aligned16(q_nope) || !aligned16(q_pe) || !aligned16(wkv_b) || !aligned16(O))
     return MLA_ERR_ALIGN;
   if (!ws || !aligned256(ws)) return MLA_ERR_WORKSPACE;
   if (int e = check_device()) return e;
-  if (ws_bytes < mla_attend_paged_workspace_bytes(N, S, max_kv, form)) return MLA_ERR_WORKSPACE;
+  if (ws_bytes < mla_attend_paged_workspace_bytes(N, S, max_kv, kind, form))
+    return MLA_ERR_WORKSPACE;
   paged::Pool p;
   p.base = static_cast<const uint8_t*>(pool);
   p.kind = kind;

@@ -132,11 +132,15 @@ __global__ void __launch_bounds__(1024) layout_kernel(const Seqs q, const Pool p
 // ===========================================================================
 // gather: row ly.row[s] + t = position t of sequence s as bf16, zeros from
 // kv[s] to the next multiple of 128 and for entries outside the pool (counted
-// once a page).  One warp per row; bound by memory.
+// once a page).  One warp per row; bound by memory.  `table`, if there is one:
+// the rows' table as pages of 64.
 // ===========================================================================
+constexpr int kStagedPage = 64;
+
 template <bool kE4M3>
 __global__ void __launch_bounds__(256) gather_kernel(const Pool pool, const Layout ly, int S,
                                                       __nv_bfloat16* __restrict__ rows,
+                                                      int32_t* __restrict__ table, int max_pages,
                                                       int32_t* status) {
   const int lane = threadIdx.x & 31;
   const int total = ld_global_nc_s32_early(ly.row + S);
@@ -147,6 +151,8 @@ __global__ void __launch_bounds__(256) gather_kernel(const Pool pool, const Layo
       if (ly.row[m] <= r) a = m; else e = m;
     }
     const int t = r - ly.row[a];
+    if (table && lane == 0 && t % kStagedPage == 0)
+      table[(long long)a * max_pages + t / kStagedPage] = r / kStagedPage;
     uint4 x = make_uint4(0, 0, 0, 0), y = x, pe = x;
     if (t < ly.kv[a]) {
       const int row = paged::row_of(pool, pool.table + (long long)a * pool.max_pages, t);
@@ -746,27 +752,40 @@ __global__ void __launch_bounds__(attn::THREADS, 1)
 // host
 // ===========================================================================
 
-struct Ws {
-  size_t row, kv, block, count, rows, k, v, total;
+// The first part of a workspace: the layout and the gathered rows.
+struct RowsWs {
+  size_t row, kv, block, count, rows, total;
   int64_t max_rows;
-  int heads;  // of a group
 };
 
-static Ws layout(int N, int S, int max_kv) {
-  Ws w;
+static RowsWs rows_ws(int N, int S, int max_kv) {
+  RowsWs w;
   // (a pair's second CTA may reach 128 rows past the last sequence)
   w.max_rows = (int64_t)S * ((max_kv + kRows - 1) / kRows * kRows);
   w.max_rows = (w.max_rows + 2 * kRows - 1) / (2 * kRows) * (2 * kRows);
-  w.heads = kH;
-  while (w.heads > 8 && (size_t)w.max_rows * w.heads * 2 * kD * 2 > kGroupBytes) w.heads /= 2;
   w.row = 0;
   w.kv = round_up((size_t)(S + 1) * 4, 256);
   w.block = round_up(w.kv + (size_t)S * 4, 256);
   w.count = round_up(w.block + ((size_t)N / kBlock + S) * sizeof(Block), 256);
   w.rows = w.count + 256;
-  w.k = round_up(w.rows + (size_t)w.max_rows * MLA_ROW * 2, 256);
-  w.v = w.k + (size_t)w.max_rows * w.heads * kD * 2;
-  w.total = w.v + (size_t)w.max_rows * w.heads * kD * 2;
+  w.total = round_up(w.rows + (size_t)w.max_rows * MLA_ROW * 2, 256);
+  return w;
+}
+
+struct Ws {
+  RowsWs r;
+  size_t k, v, total;
+  int heads;  // of a group
+};
+
+static Ws layout(int N, int S, int max_kv) {
+  Ws w;
+  w.r = rows_ws(N, S, max_kv);
+  w.heads = kH;
+  while (w.heads > 8 && (size_t)w.r.max_rows * w.heads * 2 * kD * 2 > kGroupBytes) w.heads /= 2;
+  w.k = w.r.total;
+  w.v = w.k + (size_t)w.r.max_rows * w.heads * kD * 2;
+  w.total = w.v + (size_t)w.r.max_rows * w.heads * kD * 2;
   return w;
 }
 
@@ -776,34 +795,73 @@ bool fits(int S, int max_kv) {
 
 size_t workspace_bytes(int N, int S, int max_kv) { return layout(N, S, max_kv).total; }
 
+static Layout make_layout(const RowsWs& w, uint8_t* ws) {
+  Layout ly;
+  ly.row = reinterpret_cast<int32_t*>(ws + w.row);
+  ly.kv = reinterpret_cast<int32_t*>(ws + w.kv);
+  ly.block = reinterpret_cast<Block*>(ws + w.block);
+  ly.count = reinterpret_cast<int32_t*>(ws + w.count);
+  return ly;
+}
+
+// layout_kernel and gather_kernel
+static int gather_rows(const RowsWs& w, const Pool& pool, const Seqs& q, uint8_t* ws,
+                       int32_t* table, int max_pages, int sms, int32_t* status, cudaStream_t st) {
+  const Layout ly = make_layout(w, ws);
+  __nv_bfloat16* rows = reinterpret_cast<__nv_bfloat16*>(ws + w.rows);
+  int shift = 0;  // key tiles of a query block into 1024 classes
+  while ((2 * ((q.max_kv + kRows - 1) / kRows) >> shift) > 1023) ++shift;
+  layout_kernel<<<1, 1024, 0, st>>>(q, pool, ly, shift);
+  if (int e = launch_status()) return e;
+  const int64_t want = (w.max_rows + 7) / 8;
+  const int blocks = (int)(want < sms * 32 ? want : sms * 32);
+  if (pool.kind == MLA_PAGE_E4M3)
+    gather_kernel<true><<<blocks, 256, 0, st>>>(pool, ly, q.S, rows, table, max_pages, status);
+  else
+    gather_kernel<false><<<blocks, 256, 0, st>>>(pool, ly, q.S, rows, table, max_pages, status);
+  return launch_status();
+}
+
+static int staged_pages(int max_kv) {
+  return (max_kv + kRows - 1) / kRows * (kRows / kStagedPage);
+}
+
+size_t staged_bytes(int N, int S, int max_kv) {
+  return rows_ws(N, S, max_kv).total + round_up((size_t)S * staged_pages(max_kv) * 4, 256);
+}
+
+int stage(const Pool& pool, const Seqs& q, uint8_t* ws, int32_t* status, cudaStream_t st,
+          Pool* staged) {
+  const RowsWs w = rows_ws(q.N, q.S, q.max_kv);
+  int sms = 0;
+  if (int e = check_device(&sms)) return e;
+  int32_t* table = reinterpret_cast<int32_t*>(ws + w.total);
+  staged->base = ws + w.rows;
+  staged->kind = MLA_PAGE_BF16;
+  staged->num_pages = (int)(w.max_rows / kStagedPage);
+  staged->page_size = staged->pitch = kStagedPage;
+  staged->row_stride = MLA_ROW * 2;
+  staged->rows = (int)w.max_rows;
+  staged->table = table;
+  staged->max_pages = staged_pages(q.max_kv);
+  paged::set_division(staged);
+  return gather_rows(w, pool, q, ws, table, staged->max_pages, sms, status, st);
+}
+
 int run(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const mla_bf16_t* wkv_b,
         const paged::Pool& pool, const paged::Seqs& q, float scale, mla_bf16_t* O, uint8_t* ws,
         int32_t* status, cudaStream_t st) {
   const Ws L = layout(q.N, q.S, q.max_kv);
   int sms = 0;
   if (int e = check_device(&sms)) return e;
-  Layout ly;
-  ly.row = reinterpret_cast<int32_t*>(ws + L.row);
-  ly.kv = reinterpret_cast<int32_t*>(ws + L.kv);
-  ly.block = reinterpret_cast<Block*>(ws + L.block);
-  ly.count = reinterpret_cast<int32_t*>(ws + L.count);
-  __nv_bfloat16* rows = reinterpret_cast<__nv_bfloat16*>(ws + L.rows);
+  if (int e = gather_rows(L.r, pool, q, ws, nullptr, 0, sms, status, st)) return e;
+  const Layout ly = make_layout(L.r, ws);
+  __nv_bfloat16* rows = reinterpret_cast<__nv_bfloat16*>(ws + L.r.rows);
   __nv_bfloat16* k = reinterpret_cast<__nv_bfloat16*>(ws + L.k);
   __nv_bfloat16* v = reinterpret_cast<__nv_bfloat16*>(ws + L.v);
-  int shift = 0;  // key tiles of a query block into 1024 classes
-  while ((2 * ((q.max_kv + kRows - 1) / kRows) >> shift) > 1023) ++shift;
-  layout_kernel<<<1, 1024, 0, st>>>(q, pool, ly, shift);
-  if (int e = launch_status()) return e;
-  const int64_t want = (L.max_rows + 7) / 8;
-  const int blocks = (int)(want < sms * 32 ? want : sms * 32);
-  if (pool.kind == MLA_PAGE_E4M3)
-    gather_kernel<true><<<blocks, 256, 0, st>>>(pool, ly, q.S, rows, status);
-  else
-    gather_kernel<false><<<blocks, 256, 0, st>>>(pool, ly, q.S, rows, status);
-  if (int e = launch_status()) return e;
 
   alignas(64) CUtensorMap map_c, map_w, map_k, map_v, map_r, map_qn, map_qr;
-  const uint64_t R = (uint64_t)L.max_rows;
+  const uint64_t R = (uint64_t)L.r.max_rows;
   if (int e = bf16_map_2d(&map_c, rows, kC, R, MLA_ROW * 2, 64, kRows)) return e;
   if (int e = bf16_map_2d(&map_w, wkv_b, kC, kH * 256, kC * 2, 64, 128)) return e;
   if (int e = bf16_map_3d(&map_k, k, kD, R, L.heads, kD * 2, R * kD * 2, 64, kRows, 1)) return e;

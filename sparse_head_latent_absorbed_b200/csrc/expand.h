@@ -16,6 +16,12 @@ bool fits(int S, int max_kv);
 
 size_t workspace_bytes(int N, int S, int max_kv);
 
+// The rows of a call's sequences as bf16, one sequence after another in pages of
+// 64: a pool and table that the absorbed form reads instead of 8-bit pages.
+size_t staged_bytes(int N, int S, int max_kv);
+int stage(const paged::Pool& pool, const paged::Seqs& q, uint8_t* ws, int32_t* status,
+          cudaStream_t st, paged::Pool* staged);
+
 int run(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const mla_bf16_t* wkv_b,
         const paged::Pool& pool, const paged::Seqs& q, float scale, mla_bf16_t* O, uint8_t* ws,
         int32_t* status, cudaStream_t st);

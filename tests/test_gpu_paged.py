@@ -218,6 +218,41 @@ def test_lengths_are_cut_to_the_bound_and_the_table(shla, form):
     check(got, ref_of(w))
 
 
+@pytest.mark.parametrize("page", [64, 48, 1])
+def test_8_bit_pages_that_several_tokens_read(shla, page):
+    # (the absorbed form reads them once for all tokens of a call of this size)
+    q, kv = [5, 1, 0, 3, 60], [7000, 129, 50, 2, 640]
+    w = R.make(q, kv, 8, page, 20, pad_tokens=1)
+    w["page_table"][1, 0] = -1
+    out = torch.full_like(w["q_nope"], 7.0)
+    status = torch.zeros(2, dtype=torch.int32, device="cuda")
+    shla.mla_attend_paged(**w, form="absorbed", out=out, status=status)
+    assert status.tolist() == [0, 1] and (out[69:] == 7).all()
+    check(out[:69], ref_of(w)[:69])
+    # lengths beyond a table that is shorter than the bound
+    keep = 6720 // page
+    w["page_table"] = w["page_table"][:, :keep].contiguous()
+    w["max_kv"] = 9000
+    got = shla.mla_attend_paged(**w, form="absorbed")
+    w["kv_len"] = w["kv_len"].clamp(max=keep * page)
+    check(got[:69], ref_of(w)[:69])
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("q,kv", [([1] * 3, [700, 64, 130]), ([2, 130], [300, 260])])
+def test_scales_of_every_size(shla, form, q, kv):
+    # groups whose scales lie near 2^20, 2^-100, 1 and 2^9: wkv_b makes up for
+    # the width, so that the scores stay as they are
+    w = R.make(q, kv, 8, 16, 21, poison=False)
+    flat = R.values(w["pages"].view(-1, 656))
+    wide = torch.tensor([2.0 ** 20, 2.0 ** -100, 1.0, 2.0 ** 9], dtype=torch.float64,
+                        device="cuda").repeat_interleave(128)
+    flat[:, :512] *= wide
+    w["pages"] = R.row8(flat.to(torch.bfloat16)).view(w["pages"].shape)
+    w["wkv_b"] = (w["wkv_b"].double() / wide).to(torch.bfloat16)
+    check(shla.mla_attend_paged(**w, form=form), ref_of(w))
+
+
 @pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("factor", [10.0, 0.01])
 def test_wide_and_narrow_scores(shla, form, factor):
@@ -282,7 +317,7 @@ def test_captured_call_follows_its_inputs(shla, form):
     keep = {k: a[k].clone() for k in ("q_nope", "q_pe", "page_table", "cu_q", "kv_len", "pages")}
     N, S = a["q_nope"].shape[0], 3
     a["max_kv"] = 700
-    ws = torch.empty(shla.mla_attend_paged_workspace_bytes(N, S, 700, form), dtype=torch.uint8,
+    ws = torch.empty(shla.mla_attend_paged_workspace_bytes(N, S, 700, 8, form), dtype=torch.uint8,
                      device="cuda")
     out = torch.full_like(a["q_nope"], 7.0)
     shla.mla_attend_paged(**a, form=form, out=out, ws=ws)

@@ -60,17 +60,24 @@ def test_attend(L):
 
 def test_workspace_sizes(L):
     f = L.mla_attend_paged_workspace_bytes
-    assert f(0, 1, 10) == f(1, 0, 10) == f(1, 1, 0) == 0
+    assert f(0, 1, 10, 16) == f(1, 0, 10, 16) == f(1, 1, 0, 16) == 0
     # q~ and the mixed latents of each token, two partial ones for each SM pair
-    assert f(16, 16, 100, "absorbed") >= 2 * 16 * 128 * 512 * 2 + 2 * 128 * 512 * 2
+    own = f(16, 16, 100, 16, "absorbed")
+    assert own >= 2 * 16 * 128 * 512 * 2 + 2 * 128 * 512 * 2
+    # 8-bit pages that several tokens a sequence read are staged as bf16 rows
+    assert f(16, 16, 100, 8, "absorbed") == own == f(16, 5, 100, 8, "absorbed")
+    assert f(16, 5, 16384, 8, "absorbed") >= own + 5 * 16384 * 1152
+    assert own == f(16, 6, 16384, 8, "absorbed") == f(16, 5, 16383, 8, "absorbed")
+    assert own == f(16, 5, 16384, 16, "absorbed") == f(16, 5, 1 << 20, 8, "absorbed")
     # keys and values of 128 heads, of fewer where they would pass 4 GiB
-    assert f(128, 1, 128) >= 256 * (1152 + 128 * 512)
-    assert f(512, 1, 2 ** 17) < 2 ** 17 * 1152 + 2 ** 32 + 2 ** 20
+    assert f(128, 1, 128, 8) >= 256 * (1152 + 128 * 512)
+    assert f(512, 1, 2 ** 17, 16) < 2 ** 17 * 1152 + 2 ** 32 + 2 ** 20
     # the form that "auto" takes
-    assert f(127, 1, 500) == f(127, 1, 500, "absorbed") != f(127, 1, 500, "expanded")
-    assert f(128, 1, 500) == f(128, 1, 500, "expanded")
-    with pytest.raises(L.MLAError):
-        f(1, 1, 10, "other")
+    assert f(127, 1, 500, 16) == f(127, 1, 500, 16, "absorbed") != f(127, 1, 500, 16, "expanded")
+    assert f(128, 1, 500, 16) == f(128, 1, 500, 16, "expanded")
+    for bad in (dict(form="other"), dict(bits=4)):
+        with pytest.raises(L.MLAError):
+            f(1, 1, 10, **{"bits": 16, **bad})
 
 
 def test_scale(L):

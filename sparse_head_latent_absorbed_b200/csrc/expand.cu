@@ -8,7 +8,7 @@
 // 278,528, for 33.6 Mflop a position.  Four kernels:
 //
 //   layout_kernel   one block: where each sequence's positions go, and the list
-//                   of 256-token query blocks, heaviest first
+//                   of query blocks (up to 512 tokens), heaviest first
 //   gather_kernel   the pages' rows, as bf16, one sequence after another
 //   expand_kernel   K and V of a group of heads: a GEMM on CTA pairs
 //   chunk_kernel    the attention of the group's heads
@@ -30,19 +30,34 @@ using paged::kR;
 using paged::Pool;
 using paged::Seqs;
 
-constexpr int kRows = 128;     // positions of a key tile, tokens of a query tile
-constexpr int kBlock = 256;    // tokens of a query block (two tiles)
+constexpr int kRows = 128;     // positions of a key tile, tokens of a CTA's query tile
+constexpr int kTile = 256;     // tokens of a pair's query tile
+constexpr int kBlock = 512;    // tokens of a query block
 constexpr size_t kGroupBytes = size_t(4) << 30;  // keys and values of a group of heads
 
 // ===========================================================================
 // layout
 // ===========================================================================
 
-// A query block: tokens [tok, tok + n) of one sequence; the first sees `lim`
-// positions (possibly none or less), each next one more, none more than kv;
-// position 0 is row `row` of the gathered rows.
+// A query block: tokens [tok, tok + n) of one sequence, n <= 512; the first sees
+// `lim` positions (possibly none or less), each next one more, none more than kv;
+// position 0 is row `row` of the gathered rows.  A CTA pair works on two query
+// tiles at a time: of up to 256 tokens, the same block for two heads; of more,
+// both parts of the block for one head, and the list has the block twice, for the
+// first and for the second half of the heads (`upper`).
 struct Block {
-  int tok, n, lim, kv, row;
+  int tok, n, lim, kv, row, upper;
+  DEV bool two_heads() const { return n <= kTile; }
+  // tokens of a tile that each CTA takes
+  DEV int width() const { return two_heads() ? (n + 1) / 2 : (n + 3) / 4; }
+  DEV int first(int t) const { return two_heads() ? 0 : t * 2 * width(); }  // of tile t
+  DEV int head(int t, int i, int heads) const {  // item i of heads / 2
+    return two_heads() ? 2 * i + t : upper * (heads / 2) + i;
+  }
+  DEV int tiles(int t) const {  // key tiles of query tile t
+    const int last = min(n, first(t) + 2 * width());
+    return max(0, (min(kv, lim + last - 1) + kRows - 1) / kRows);
+  }
 };
 
 struct Layout {
@@ -51,13 +66,6 @@ struct Layout {
   Block* block;    // [N / 256 + S]
   int32_t* count;  // [1] blocks
 };
-
-DEV int tiles_of(const Block& b, int t) {  // key tiles of query tile t
-  const int n = min(b.n - t * kRows, kRows);
-  if (n <= 0) return 0;
-  const int lim = min(b.kv, b.lim + t * kRows + n - 1);
-  return max(0, (lim + kRows - 1) / kRows);
-}
 
 // exclusive prefix sum over the block's 1024 threads; *total: the sum
 DEV int scan1024(int v, int* part, int* total) {
@@ -109,7 +117,11 @@ __global__ void __launch_bounds__(1024) layout_kernel(const Seqs q, const Pool p
         b.kv = ly.kv[s];
         b.lim = b.kv - n + i + 1;
         b.row = ly.row[s];
-        const int w = (tiles_of(b, 0) + tiles_of(b, 1)) >> classes_shift;
+        b.upper = 0;
+        const int w = (b.tiles(0) + b.tiles(1)) >> classes_shift;
+        f(b, 1023 - min(1023, w));
+        if (b.two_heads()) continue;
+        b.upper = 1;
         f(b, 1023 - min(1023, w));
       }
     }
@@ -120,7 +132,7 @@ __global__ void __launch_bounds__(1024) layout_kernel(const Seqs q, const Pool p
   const int first = scan1024(mine, part, &total);
   cls[tid] = first;
   // (ranges of a cu_q that decreases may overlap: no more blocks than there is room for)
-  const int room = q.N / kBlock + q.S;
+  const int room = q.N / kTile + q.S;
   if (tid == 0) *ly.count = min(total, room);
   __syncthreads();
   each([&](const Block& b, int c) {
@@ -381,7 +393,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm::THREADS, 1)
         fence_proxy_async_smem();
         asm volatile("bar.sync 1, 128;" ::: "memory");
         if (tid == 0) {
-          tma_store_3d(b < 2 ? &map_k : &map_v, (b & 1) * 64, rb * 2 * kRows + rank * kRows, h, box);
+          tma_store_3d(b < 2 ? &map_k : &map_v, 0, rb * 2 * kRows + rank * kRows, 2 * h + (b & 1),
+                       box);
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
       }
@@ -406,43 +419,87 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm::THREADS, 1)
 }
 
 // ===========================================================================
-// chunk_kernel: attention of a query block (two tiles of 128 tokens) of one
-// head over its sequence's key tiles of 128 positions
-//   S_t = Q_t K^T   M = 128 tokens, N = 128, K = 192, both from shared memory
-//   O_t += P_t V    M = 128, N = 2 x 64, K = 128, P from TMEM
-// with one fp32 online softmax per token (a thread per token: no shuffles).
-// Two query tiles share every key tile: while one's scores are in the softmax
-// the tensor cores work for the other.  P overlays its scores, rounded to bf16
-// as a tensor-core operand (the row sum is of the fp32 weights).
-// Warps 0-3 and 4-7: softmax and output of tile 0 and 1; warp 8: TMA; warp 9:
-// MMA.  Keys and values arrive in 16 KB units (64 columns of 128 positions;
-// key: two of the non-rotary part and one rotary, value: two) through a ring
-// of eight.
+// chunk_kernel: attention of two query tiles over the key tiles of 128 positions
+//   S_t = Q_t K^T   K = 192, both from shared memory
+//   O_t += P_t V    K = 128, P from TMEM
+// A pair of CTAs (tcgen05 cta_group::2, M = 256, N = 128) holds 128 rows of each
+// query tile in each CTA, and of the keys and values each CTA half: 64 positions
+// of a key tile, 64 columns of a value tile.  One CTA alone (M = 128) reads 8 KB
+// of operands for the 64 cycles of a score product, all that shared memory gives;
+// then every wait and every load held up the products (measured: 2060 cycles a
+// tile instead of the 1290 it computes; of the pair 6 KB).
+// One fp32 online softmax per token, a thread each: no shuffles.  While one
+// query tile's scores are in the softmax the tensor cores work for the other;
+// the first half of the keys' weights is multiplied while the second half is
+// still being computed.  P overlays its scores, rounded to bf16 as a tensor-core
+// operand (the row sum is of the fp32 weights).
+// Warps 0-3 and 4-7: softmax and output of tile 0 and 1; warp 8: queries and
+// keys by TMA; warp 9: MMA (of the pair's first CTA); warp 10: values by TMA.
 // TMEM: scores [0,128) [128,256), outputs [256,384) [384,512).
 // ===========================================================================
 namespace attn {
-constexpr int UNIT = kRows * 128;
-constexpr int NU = 8;
-constexpr int OFF_U = 6 * UNIT;  // after two query tiles of three units
-constexpr int SMEM = OFF_U + NU * UNIT + 1024;
-constexpr int THREADS = 384;  // (two idle warps complete the third register group)
+constexpr int Q_BYTES = 3 * kRows * 128;   // a query tile, in three columns of 64
+constexpr int K_BYTES = 3 * 64 * 128;      // 64 positions
+constexpr int V_BYTES = kRows * 128;       // 64 columns
+constexpr int NK = 3, NV = 3;              // ring depths
+constexpr int OFF_K = 2 * Q_BYTES;
+constexpr int OFF_V = OFF_K + NK * K_BYTES;
+constexpr int SMEM = OFF_V + NV * V_BYTES + 1024;
+constexpr int THREADS = 384;  // (an idle warp completes the third register group)
 // register split (168 per thread at launch): 2 x 208 + 88 = 3 x 168
 constexpr int REGS_SOFT = 208, REGS_REST = 88;
 static_assert(2 * REGS_SOFT + REGS_REST <= 3 * 168, "register split");
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 static_assert(SMEM + 512 <= 232448, "shared memory budget");
 
-struct Bars {
-  uint64_t q_full[2], q_free[2];
-  uint64_t full[NU], empty[NU];
-  uint64_t s_full[2], p_full[2], o_full[2];
+struct Bars {  // "first": waited on by the first CTA; "both": committed to both
+  uint64_t q_full[2], q_free[2];     // first / both
+  uint64_t k_full[NK], k_empty[NK];  // first / both
+  uint64_t v_full[NV], v_empty[NV];  // first / both
+  uint64_t s_full[2], o_full[2];     // both
+  uint64_t p_full[2][2];             // first: by tile and half of the keys
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
 };
+
+// which of eight pairs of weights are computed without the exponential unit
+constexpr uint32_t kByPolynomial = 0x00;
+
+// 2^x of two x: x = n + f with n the nearest whole number, 2^f by the cubic with
+// the least largest relative error over [-1/2, 1/2] (7.5e-5, found by Remez'
+// exchange; a bf16 rounding of the weight is off by up to 3.9e-3), n added to its
+// exponent.  x below -126 counts as -126.
+DEV void exp2_cubic(float& x, float& y) {
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x));
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(y));
+  const uint64_t v = pack2(x, y);
+  const uint64_t big = pack2(12582912.f, 12582912.f), nbig = pack2(-12582912.f, -12582912.f);
+  const uint64_t r = add2(v, big);  // n in the low bits
+  const uint64_t f = fma2(add2(r, nbig), pack2(-1.f, -1.f), v);
+  uint64_t p = fma2(f, pack2(0.05517167f, 0.05517167f), pack2(0.24261113f, 0.24261113f));
+  p = fma2(p, f, pack2(0.693260968f, 0.693260968f));
+  p = fma2(p, f, pack2(0.999928057f, 0.999928057f));
+  float rx, ry, px, py;
+  unpack2(r, rx, ry);
+  unpack2(p, px, py);
+  x = u2f(f2u(px) + (f2u(rx) << 23));
+  y = u2f(f2u(py) + (f2u(ry) << 23));
+}
 }  // namespace attn
 
-__global__ void __launch_bounds__(attn::THREADS, 1)
+// D (+)= A B with A in TMEM: each CTA of the pair its own rows at the same address
+template <bool kAccumulate>
+DEV void tc_mma2_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "n"(kAccumulate ? 1 : 0)
+      : "memory");
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_constant__ CUtensorMap map_qr,
                  const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_r,
                  const __grid_constant__ CUtensorMap map_v, const Layout ly, int head0, int heads,
@@ -453,193 +510,215 @@ __global__ void __launch_bounds__(attn::THREADS, 1)
   const uint32_t sbase = smem_u32(smem);
   __shared__ Bars bars;
   volatile int* abort = &bars.abort;
+  const uint32_t rank = cluster_ctarank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int items = ld_global_nc_s32_early(ly.count) * heads;
+  const int per = heads / 2;  // items of a block
+  const int items = ld_global_nc_s32_early(ly.count) * per;
+  const int it0 = blockIdx.x >> 1, step = gridDim.x >> 1;
 
-  if (warp == 9) {
-    tmem_alloc(&bars.tmem_base, 512);
-    tmem_relinquish();
-  }
+  if (warp == 9) tmem_alloc2(&bars.tmem_base, 512);
   if (tid == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars.q_full[t], 1);
       mbar_init(&bars.q_free[t], 1);
       mbar_init(&bars.s_full[t], 1);
-      mbar_init(&bars.p_full[t], 4);
+      mbar_init(&bars.p_full[t][0], 8);  // four warps of each CTA
+      mbar_init(&bars.p_full[t][1], 8);
       mbar_init(&bars.o_full[t], 1);
     }
-    for (int i = 0; i < NU; ++i) {
-      mbar_init(&bars.full[i], 1);
-      mbar_init(&bars.empty[i], 1);
+    for (int i = 0; i < NK; ++i) {
+      mbar_init(&bars.k_full[i], 1);
+      mbar_init(&bars.k_empty[i], 1);
+    }
+    for (int i = 0; i < NV; ++i) {
+      mbar_init(&bars.v_full[i], 1);
+      mbar_init(&bars.v_empty[i], 1);
     }
     mbar_init(&bars.drain, 1);
     bars.abort = 0;
     fence_mbarrier_init_cluster();
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
 
-  if (warp >= 10) {
+  if (warp == 11) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));  // (idle)
   } else if (warp == 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
-    // ---------------- TMA ----------------
+    // ---------------- queries and keys: each CTA its own, counted by the first ----------------
+    const uint32_t q_full0 = mapa_shared(smem_u32(&bars.q_full[0]), 0);
+    const uint32_t k_full0 = mapa_shared(smem_u32(&bars.k_full[0]), 0);
     int u = 0, qn[2] = {0, 0};
     bool ok = true;
-    auto unit = [&](const CUtensorMap* map, int x, int y, int z, bool three) {
-      ok = ok && warp_wait(&bars.empty[u % NU], ((u / NU) & 1) ^ 1, abort, status);
-      if (!ok) return;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bars.full[u % NU], UNIT);
-        const uint32_t dst = sbase + OFF_U + (u % NU) * UNIT;
-        if (three) tma_load_3d(dst, map, x, y, z, &bars.full[u % NU]);
-        else tma_load_2d(dst, map, x, y, &bars.full[u % NU]);
-      }
-      ++u;
-    };
-    for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
-      const int h = it % heads;
-      const Block b = ly.block[it / heads];
-      const int nt[2] = {tiles_of(b, 0), tiles_of(b, 1)};
-      const int n = max(nt[0], nt[1]);
+    for (int it = it0; it < items && ok; it += step) {
+      const Block b = ly.block[it / per];
+      const int nt[2] = {b.tiles(0), b.tiles(1)};
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (nt[t] == 0) continue;
         ok = ok && warp_wait(&bars.q_free[t], (qn[t] & 1) ^ 1, abort, status);
         if (!ok) break;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&bars.q_full[t], 3 * UNIT);
-          const uint32_t dst = sbase + t * 3 * UNIT;
-          tma_load_3d(dst, &map_qn, 0, head0 + h, b.tok + t * kRows, &bars.q_full[t]);
-          tma_load_3d(dst + UNIT, &map_qn, 64, head0 + h, b.tok + t * kRows, &bars.q_full[t]);
-          tma_load_3d(dst + 2 * UNIT, &map_qr, 0, head0 + h, b.tok + t * kRows, &bars.q_full[t]);
+          if (rank == 0) mbar_arrive_expect_tx(&bars.q_full[t], 2 * Q_BYTES);
+          const uint32_t dst = sbase + t * Q_BYTES, bar = q_full0 + t * 8;
+          const int h = head0 + b.head(t, it % per, heads);
+          const int tok = b.tok + b.first(t) + rank * b.width();
+          tma_load_3d_pair(dst, &map_qn, 0, h, tok, bar);
+          tma_load_3d_pair(dst + Q_BYTES / 3, &map_qn, 64, h, tok, bar);
+          tma_load_3d_pair(dst + Q_BYTES / 3 * 2, &map_qr, 0, h, tok, bar);
         }
         ++qn[t];
       }
-      for (int j = 0; j < n && ok; ++j) {
-        const int r = b.row + j * kRows;
-        unit(&map_k, 0, r, h, true);
-        unit(&map_k, 64, r, h, true);
-        unit(&map_r, 0, r, 0, false);
-        unit(&map_v, 0, r, h, true);
-        unit(&map_v, 64, r, h, true);
-      }
+      const int two = b.two_heads();
+      for (int j = 0; j < nt[1] && ok; ++j)
+        for (int t = two ? 0 : 1; t < 2; ++t) {
+          const int s = u % NK;
+          ok = ok && warp_wait(&bars.k_empty[s], ((u / NK) & 1) ^ 1, abort, status);
+          if (!ok) break;
+          if (lane == 0) {
+            if (rank == 0) mbar_arrive_expect_tx(&bars.k_full[s], 2 * K_BYTES);
+            const uint32_t dst = sbase + OFF_K + s * K_BYTES;
+            const int r = b.row + j * kRows + rank * 64;
+            tma_load_3d_pair(dst, &map_k, 0, r, 2 * b.head(t, it % per, heads), k_full0 + s * 8);
+            tma_load_2d_pair(dst + K_BYTES / 3 * 2, &map_r, 0, r, k_full0 + s * 8);
+          }
+          ++u;
+        }
     }
-    // on an abort, the loads still in flight land before the CTA can leave
-    for (int i = max(0, u - NU); i < u; ++i)
-      warp_wait(&bars.full[i % NU], (i / NU) & 1, nullptr, nullptr);
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-      if (qn[t]) warp_wait(&bars.q_full[t], (qn[t] - 1) & 1, nullptr, nullptr);
+    __syncwarp();
+  } else if (warp == 10) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
+    // ---------------- values ----------------
+    const uint32_t v_full0 = mapa_shared(smem_u32(&bars.v_full[0]), 0);
+    int u = 0;
+    bool ok = true;
+    for (int it = it0; it < items && ok; it += step) {
+      const Block b = ly.block[it / per];
+      const int n = b.tiles(1), two = b.two_heads();
+      for (int j = 0; j < n && ok; ++j)
+        for (int t = two ? 0 : 1; t < 2; ++t) {
+          const int s = u % NV;
+          ok = ok && warp_wait(&bars.v_empty[s], ((u / NV) & 1) ^ 1, abort, status);
+          if (!ok) break;
+          if (lane == 0) {
+            if (rank == 0) mbar_arrive_expect_tx(&bars.v_full[s], 2 * V_BYTES);
+            tma_load_3d_pair(sbase + OFF_V + s * V_BYTES, &map_v, 0, b.row + j * kRows,
+                             2 * b.head(t, it % per, heads) + rank, v_full0 + s * 8);
+          }
+          ++u;
+        }
+    }
+    __syncwarp();
   } else if (warp == 9) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
     // ---------------- MMA ----------------
-    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
-    constexpr uint32_t idesc_o = idesc_bf16_f32(128, 64, 0, 1);
-    constexpr uint32_t hi128 = desc_hi(1024, kSwizzle128B);
-    int u0 = 0;                     // ring position of the item's first unit
-    int qn[2] = {0, 0}, pn[2] = {0, 0};
-    bool ok = true;
-    auto have = [&](int u) {
-      return warp_wait(&bars.full[u % NU], (u / NU) & 1, abort, status);
-    };
-    // scores of query tile t and key tile at units u .. u+2; `done`: the
-    // key tile's last use; `lastq`: the query tile's last use
-    auto score = [&](int t, int u, bool done, bool lastq) {
-#pragma unroll
-      for (int c = 0; c < 3; ++c) {
-        ok = ok && have(u + c);
+    if (rank == 0) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(256, 128, 0, 0);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(256, 128, 0, 1);
+      constexpr uint32_t hi128 = desc_hi(1024, kSwizzle128B);
+      int u0 = 0;  // ring position of the item's first tile
+      int qn[2] = {0, 0}, pn[2] = {0, 0};
+      bool ok = true;
+      // scores of query tile t and the key tile at ring position u; `done`: its
+      // last use; `lastq`: the query tile's last use
+      auto score = [&](int t, int u, bool done, bool lastq) {
+        const int s = u % NK;
+        ok = ok && warp_wait(&bars.k_full[s], (u / NK) & 1, abort, status);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t al = desc_lo(sbase + (t * 3 + c) * UNIT, 16);
-        const uint32_t bl = desc_lo(sbase + OFF_U + ((u + c) % NU) * UNIT, 16);
+        const uint32_t al = desc_lo(sbase + t * Q_BYTES, 16);
+        const uint32_t bl = desc_lo(sbase + OFF_K + s * K_BYTES, 16);
         if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            tc_mma(tmem + t * 128, desc_join(al + ks * 2, hi128), desc_join(bl + ks * 2, hi128),
-                   idesc_s, (c > 0 || ks > 0) ? 1u : 0u);
-          if (done) tc_commit(&bars.empty[(u + c) % NU]);
+          for (int c = 0; c < 3; ++c)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              tc_mma2(tmem + t * 128, desc_join(al + c * (Q_BYTES / 48) + ks * 2, hi128),
+                      desc_join(bl + c * (K_BYTES / 48) + ks * 2, hi128), idesc_s,
+                      (c > 0 || ks > 0) ? 1u : 0u);
+          tc_commit2(&bars.s_full[t]);
+          if (done) tc_commit2(&bars.k_empty[s]);
+          if (lastq) tc_commit2(&bars.q_free[t]);
         }
         __syncwarp();
-      }
-      if (elect_one()) {
-        tc_commit(&bars.s_full[t]);
-        if (lastq) tc_commit(&bars.q_free[t]);
-      }
-      __syncwarp();
-    };
-    auto value = [&](int t, int u, bool first, bool done, bool last) {
-      ok = ok && warp_wait(&bars.p_full[t], pn[t] & 1, abort, status);
-      ++pn[t];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        ok = ok && have(u + c);
+      };
+      auto value = [&](int t, int u, bool first, bool done, bool last) {
+        const int s = u % NV;
+        ok = ok && warp_wait(&bars.v_full[s], (u / NV) & 1, abort, status);
+        const uint32_t bl = desc_lo(sbase + OFF_V + s * V_BYTES, V_BYTES);
+        const uint32_t d = tmem + 256 + t * 128, a = tmem + t * 128;
+        ok = ok && warp_wait(&bars.p_full[t][0], pn[t] & 1, abort, status);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t bl = desc_lo(sbase + OFF_U + ((u + c) % NU) * UNIT, UNIT);
-        const uint32_t d = tmem + 256 + t * 128 + c * 64, a = tmem + t * 128;
         if (elect_one()) {
-          if (first) tc_mma_tmem_a_c<false>(d, a, desc_join(bl, hi128), idesc_o);
-          else tc_mma_tmem_a_c<true>(d, a, desc_join(bl, hi128), idesc_o);
+          if (first) tc_mma2_tmem_a<false>(d, a, desc_join(bl, hi128), idesc_o);
+          else tc_mma2_tmem_a<true>(d, a, desc_join(bl, hi128), idesc_o);
 #pragma unroll
-          for (int ks = 1; ks < 8; ++ks)
-            tc_mma_tmem_a_c<true>(d, a + ks * 8, desc_join(bl + ks * (2048 >> 4), hi128), idesc_o);
-          if (done) tc_commit(&bars.empty[(u + c) % NU]);
+          for (int ks = 1; ks < 4; ++ks)
+            tc_mma2_tmem_a<true>(d, a + ks * 8, desc_join(bl + ks * (2048 >> 4), hi128), idesc_o);
         }
         __syncwarp();
+        ok = warp_wait(&bars.p_full[t][1], pn[t] & 1, abort, status);
+        ++pn[t];
+        if (!ok) return;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 4; ks < 8; ++ks)
+            tc_mma2_tmem_a<true>(d, a + ks * 8, desc_join(bl + ks * (2048 >> 4), hi128), idesc_o);
+          if (done) tc_commit2(&bars.v_empty[s]);
+          if (last) tc_commit2(&bars.o_full[t]);
+        }
+        __syncwarp();
+      };
+      for (int it = it0; it < items && ok; it += step) {
+        const Block b = ly.block[it / per];
+        const int nt[2] = {b.tiles(0), b.tiles(1)};  // nt[0] <= nt[1]
+        const bool two = b.two_heads();
+        const int per_j = two ? 2 : 1;
+        auto at = [&](int t, int j) { return u0 + j * per_j + (two ? t : 0); };
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (nt[t] > 0 && ok) {
+            ok = warp_wait(&bars.q_full[t], qn[t] & 1, abort, status);
+            ++qn[t];
+            score(t, at(t, 0), two || t == 1, nt[t] == 1);
+          }
+        for (int j = 0; j < nt[1] && ok; ++j)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (j < nt[t] && ok) value(t, at(t, j), j == 0, two || t == 1, j + 1 == nt[t]);
+            if (j + 1 < nt[t] && ok) score(t, at(t, j + 1), two || t == 1, j + 2 == nt[t]);
+          }
+        u0 += nt[1] * per_j;
       }
-      if (last && elect_one()) tc_commit(&bars.o_full[t]);
+      // everything issued so far has finished before TMEM is released
+      if (elect_one()) tc_commit2(&bars.drain);
       __syncwarp();
-    };
-    for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
-      const Block b = ly.block[it / heads];
-      const int nt[2] = {tiles_of(b, 0), tiles_of(b, 1)};
-      const int n = max(nt[0], nt[1]);
-      // tile t is the last to use key tile j when the other is not active there
-      auto lastuse = [&](int t, int j) { return t == 1 || j >= nt[1]; };
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (nt[t] > 0 && ok) {
-          ok = warp_wait(&bars.q_full[t], qn[t] & 1, abort, status);
-          ++qn[t];
-          if (ok) score(t, u0, lastuse(t, 0), nt[t] == 1);
-        }
-      for (int j = 0; j < n && ok; ++j)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (j < nt[t] && ok)
-            value(t, u0 + 5 * j + 3, j == 0, lastuse(t, j), j + 1 == nt[t]);
-          if (j + 1 < nt[t] && ok)
-            score(t, u0 + 5 * (j + 1), lastuse(t, j + 1), j + 2 == nt[t]);
-        }
-      u0 += 5 * n;
+      warp_wait(&bars.drain, 0, nullptr, status);
     }
-    // everything issued so far has finished before TMEM is released
-    if (elect_one()) tc_commit(&bars.drain);
-    __syncwarp();
-    warp_wait(&bars.drain, 0, nullptr, status);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
     // ---------------- softmax and output of tile t, thread = token ----------------
     const int t = warp >> 2, q4 = warp & 3;
     const int row = q4 * 32 + lane;
     const uint32_t ts = tmem + ((uint32_t)(q4 * 32) << 16) + t * 128;
-    const uint32_t to = ts - t * 128 + 256 + t * 128;
+    const uint32_t to = ts + 256;
+    const uint32_t p_full0 = mapa_shared(smem_u32(&bars.p_full[t][0]), 0);
     int sn = 0, on = 0;
     bool ok = true;
     const uint64_t scale2 = pack2(scale_log2, scale_log2);
-    for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
-      const Block b = ly.block[it / heads];
-      const int h = it % heads;
-      const int nt = tiles_of(b, t);
-      const int mine = min(b.n - t * kRows, kRows);  // tokens of this tile
-      if (mine <= 0) continue;
-      const int lim = min(b.kv, b.lim + t * kRows + row);  // positions this token sees
-      const int lim0 = b.lim + t * kRows;                  // ... and the tile's first token
+    for (int it = it0; it < items && ok; it += step) {
+      const Block b = ly.block[it / per];
+      const int nt = b.tiles(t), w = b.width();
+      const int tok0 = b.first(t) + rank * w;  // this CTA's first token of the tile, in the block
+      const int mine = min(min(b.n, b.first(t) + 2 * w) - tok0, w);
+      const int lim0 = b.lim + tok0;            // positions that one sees
+      const int lim = min(b.kv, lim0 + row);    // ... this thread's
       float m = -INFINITY;
-      uint64_t l2 = 0;  // two partial row sums
+      uint64_t la = 0, lb = 0;  // partial row sums
 #pragma unroll 1
       for (int j = 0; j < nt; ++j) {
         ok = warp_wait(&bars.s_full[t], sn & 1, abort, status);
@@ -658,11 +737,14 @@ __global__ void __launch_bounds__(attn::THREADS, 1)
         }
         float mx[4] = {u2f(s[0]), u2f(s[1]), u2f(s[2]), u2f(s[3])};
 #pragma unroll
-        for (int c = 4; c < 128; c += 4)
+        for (int c = 4; c < 124; c += 8)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], u2f(s[c + e]));
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
-        const bool raise = mt > m + kRescaleThreshold;
+          for (int e = 0; e < 4; ++e) mx[e] = max3_nan(mx[e], u2f(s[c + e]), u2f(s[c + 4 + e]));
+        float mt = max3_nan(max3_nan(mx[0], mx[1], mx[2]), u2f(s[124]), u2f(s[125]));
+        mt = max3_nan(max3_nan(mx[3], u2f(s[126]), u2f(s[127])), mt, mt) * scale_log2;
+        // (a score that is not a number, or no finite one, spoils its row for good)
+        if (!(mt < INFINITY)) mt = NAN;
+        const bool raise = !(mt <= m + kRescaleThreshold);
         if (__any_sync(0xffffffffu, raise)) {
           // (the value products before these scores have completed with them)
           const float a = raise ? fast_exp2(m - mt) : 1.f;  // 0 at the first tile
@@ -676,9 +758,9 @@ __global__ void __launch_bounds__(attn::THREADS, 1)
               for (int e = 0; e < 32; ++e) o[e] = f2u(u2f(o[e]) * a);
               tmem_st32(to + c, o);
             }
-            float x, y;
-            unpack2(l2, x, y);
-            l2 = pack2(x * a, y * a);
+            const uint64_t a2 = pack2(a, a);
+            la = mul2(la, a2);
+            lb = mul2(lb, a2);
           }
           if (raise) m = mt;
         }
@@ -686,29 +768,35 @@ __global__ void __launch_bounds__(attn::THREADS, 1)
         const float d = m == -INFINITY ? 0.f : -m;
         const uint64_t d2 = pack2(d, d);
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          uint32_t w[32];
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w2[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             float x, y;
-            unpack2(fma2(pack2(u2f(s[2 * (c + e)]), u2f(s[2 * (c + e) + 1])), scale2, d2), x, y);
-            x = fast_exp2(x);
-            y = fast_exp2(y);
-            l2 = add2(l2, pack2(x, y));
-            w[e] = pack_bf16x2(x, y);
+            unpack2(fma2(pack2(u2f(s[2 * (c * 32 + e)]), u2f(s[2 * (c * 32 + e) + 1])), scale2, d2),
+                    x, y);
+            if (kByPolynomial >> (e & 7) & 1) {
+              exp2_cubic(x, y);
+            } else {
+              x = fast_exp2(x);
+              y = fast_exp2(y);
+            }
+            if (e & 1) la = add2(la, pack2(x, y));
+            else lb = add2(lb, pack2(x, y));
+            w2[e] = pack_bf16x2(x, y);
           }
-          tmem_st32(ts + c, w);
+          tmem_st32(ts + c * 32, w2);
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_pair(p_full0 + c * 8);
         }
-        tc_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p_full[t]);
       }
       if (!ok) break;
       float inv = 0.f;
       if (nt > 0) {
         float x, y;
-        unpack2(l2, x, y);
+        unpack2(add2(la, lb), x, y);
         const float l = x + y;
         inv = l == 0.f ? 0.f : 1.f / l;
         ok = warp_wait(&bars.o_full[t], on & 1, abort, status);
@@ -716,7 +804,8 @@ __global__ void __launch_bounds__(attn::THREADS, 1)
         if (!ok) break;
         tc_fence_after();
       }
-      __nv_bfloat16* dst = O + ((size_t)(b.tok + t * kRows + row) * kH + head0 + h) * kD;
+      __nv_bfloat16* dst = O + ((size_t)(b.tok + tok0 + row) * kH + head0 +
+                                b.head(t, it % per, heads)) * kD;
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         uint32_t o[32];
@@ -742,10 +831,19 @@ __global__ void __launch_bounds__(attn::THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (*abort) {
+    // a warp that gave up may leave loads in flight, which land within
+    // microseconds: a millisecond before the pair leaves
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000) {
+    }
+  }
+  cluster_sync_all();
   if (warp == 9) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc2(tmem, 512);
   }
+  cluster_sync_all();  // neither CTA leaves before both have released
 }
 
 // ===========================================================================
@@ -766,7 +864,7 @@ static RowsWs rows_ws(int N, int S, int max_kv) {
   w.row = 0;
   w.kv = round_up((size_t)(S + 1) * 4, 256);
   w.block = round_up(w.kv + (size_t)S * 4, 256);
-  w.count = round_up(w.block + ((size_t)N / kBlock + S) * sizeof(Block), 256);
+  w.count = round_up(w.block + ((size_t)N / kTile + S) * sizeof(Block), 256);
   w.rows = w.count + 256;
   w.total = round_up(w.rows + (size_t)w.max_rows * MLA_ROW * 2, 256);
   return w;
@@ -860,13 +958,15 @@ int run(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const mla_bf16_t* wkv_
   __nv_bfloat16* k = reinterpret_cast<__nv_bfloat16*>(ws + L.k);
   __nv_bfloat16* v = reinterpret_cast<__nv_bfloat16*>(ws + L.v);
 
-  alignas(64) CUtensorMap map_c, map_w, map_k, map_v, map_r, map_qn, map_qr;
+  alignas(64) CUtensorMap map_c, map_w, map_sk, map_k, map_v, map_r, map_qn, map_qr;
   const uint64_t R = (uint64_t)L.r.max_rows;
   if (int e = bf16_map_2d(&map_c, rows, kC, R, MLA_ROW * 2, 64, kRows)) return e;
   if (int e = bf16_map_2d(&map_w, wkv_b, kC, kH * 256, kC * 2, 64, 128)) return e;
-  if (int e = bf16_map_3d(&map_k, k, kD, R, L.heads, kD * 2, R * kD * 2, 64, kRows, 1)) return e;
-  if (int e = bf16_map_3d(&map_v, v, kD, R, L.heads, kD * 2, R * kD * 2, 64, kRows, 1)) return e;
-  if (int e = bf16_map_2d(&map_r, rows + kC, kR, R, MLA_ROW * 2, 64, kRows)) return e;
+  // keys and values: [head][half of the columns][row][64]
+  if (int e = bf16_map_3d(&map_sk, k, 64, R, 2 * L.heads, 128, R * 128, 64, kRows, 1)) return e;
+  if (int e = bf16_map_3d(&map_k, k, 64, R, 2 * L.heads, 128, R * 128, 64, 64, 2)) return e;
+  if (int e = bf16_map_3d(&map_v, v, 64, R, 2 * L.heads, 128, R * 128, 64, kRows, 1)) return e;
+  if (int e = bf16_map_2d(&map_r, rows + kC, kR, R, MLA_ROW * 2, 64, 64)) return e;
   if (int e = bf16_map_3d(&map_qn, q_nope, kD, kH, q.N, kD * 2, kH * kD * 2, 64, 1, kRows))
     return e;
   if (int e = bf16_map_3d(&map_qr, q_pe, kR, kH, q.N, kR * 2, kH * kR * 2, 64, 1, kRows)) return e;
@@ -875,9 +975,9 @@ int run(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const mla_bf16_t* wkv_
   if (int e = ensure_smem_attr(chunk_kernel, attn::SMEM, &attn_attr)) return e;
   for (int h0 = 0; h0 < kH; h0 += L.heads) {
     expand_kernel<<<2 * (sms / 2), gemm::THREADS, gemm::SMEM, st>>>(
-        map_c, map_w, map_k, map_v, ly.row + q.S, h0, L.heads, status);
+        map_c, map_w, map_sk, map_v, ly.row + q.S, h0, L.heads, status);
     if (int e = launch_status()) return e;
-    chunk_kernel<<<sms, attn::THREADS, attn::SMEM, st>>>(
+    chunk_kernel<<<2 * (sms / 2), attn::THREADS, attn::SMEM, st>>>(
         map_qn, map_qr, map_k, map_r, map_v, ly, h0, L.heads, scale * 1.4426950408889634f,
         reinterpret_cast<__nv_bfloat16*>(O), status);
     if (int e = launch_status()) return e;

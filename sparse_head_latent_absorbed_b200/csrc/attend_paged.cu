@@ -1299,9 +1299,11 @@ static int run_absorbed(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const 
 using namespace shla;
 
 // The form of a call: as asked, or by the new tokens per sequence.
-static int form_of(int form, int N, int S) {
+static int form_of(int form, int N, int S, int max_kv) {
   if (form != MLA_FORM_AUTO) return form;
-  return (int64_t)N >= (int64_t)S * expand::kMinTokens ? MLA_FORM_EXPANDED : MLA_FORM_ABSORBED;
+  return (int64_t)N >= (int64_t)S * expand::min_tokens(max_kv) && expand::fits(S, max_kv)
+             ? MLA_FORM_EXPANDED
+             : MLA_FORM_ABSORBED;
 }
 
 static int check_sizes(int N, int S, int max_kv, int kind, int form) {
@@ -1310,15 +1312,16 @@ static int check_sizes(int N, int S, int max_kv, int kind, int form) {
     return MLA_ERR_SHAPE;
   if (form < MLA_FORM_AUTO || form > MLA_FORM_EXPANDED) return MLA_ERR_SHAPE;
   // absorbed: the flattened list of (token, 128-key tile) is counted in 32 bits
-  if (form_of(form, N, S) == MLA_FORM_EXPANDED ? !expand::fits(S, max_kv)
-                                               : (int64_t)N * ((max_kv + 127) / 128) > 0x3fffffff)
+  if (form_of(form, N, S, max_kv) == MLA_FORM_EXPANDED
+          ? !expand::fits(S, max_kv)
+          : (int64_t)N * ((max_kv + 127) / 128) > 0x3fffffff)
     return MLA_ERR_SHAPE;
   return MLA_OK;
 }
 
 extern "C" size_t mla_attend_paged_workspace_bytes(int N, int S, int max_kv, int kind, int form) {
   if (check_sizes(N, S, max_kv, kind, form) != MLA_OK) return 0;
-  if (form_of(form, N, S) == MLA_FORM_EXPANDED) return expand::workspace_bytes(N, S, max_kv);
+  if (form_of(form, N, S, max_kv) == MLA_FORM_EXPANDED) return expand::workspace_bytes(N, S, max_kv);
   const size_t own = round_up(paged::absorbed_ws(N, paged::max_pairs()).total, 256);
   return own + (paged::stages(kind, N, S, max_kv) ? expand::staged_bytes(N, S, max_kv) : 0);
 }
@@ -1359,7 +1362,7 @@ extern "C" int mla_attend_paged(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe
   q.S = S;
   q.N = N;
   q.max_kv = max_kv;
-  if (form_of(form, N, S) == MLA_FORM_EXPANDED)
+  if (form_of(form, N, S, max_kv) == MLA_FORM_EXPANDED)
     return expand::run(q_nope, q_pe, wkv_b, p, q, scale, O, static_cast<uint8_t*>(ws), status,
                        as_stream(stream));
   return paged::run_absorbed(q_nope, q_pe, wkv_b, p, q, scale, O, static_cast<uint8_t*>(ws),

@@ -7,8 +7,12 @@ namespace shla {
 namespace expand {
 
 // Average new tokens per sequence from which MLA_FORM_AUTO expands.  By flops
-// alone the forms meet at 33.6e6 / (278,528 - 81,920) = 171 tokens.
-constexpr int kMinTokens = 128;
+// alone the forms meet at 33.6e6 / (278,528 - 81,920) = 171 tokens.  Measured, in
+// microseconds absorbed / expanded: 32 sequences of 300 positions, 64 new tokens
+// each 602 / 638, 96 862 / 638; 8 of 1000, 96 tokens 389 / 447, 128 487 / 421; one
+// of 2000, 128 tokens 107 / 128, 160 129 / 128; one of 6000, 160 tokens 248 / 304,
+// 256 367 / 306; one of 40000, 160 tokens 1440 / 1971, 256 2215 / 1924.
+inline int min_tokens(int max_kv) { return max_kv <= 1024 ? 112 : max_kv <= 4096 ? 160 : 208; }
 
 // Positions of all sequences, each rounded up to 128, that a call may reach.
 constexpr int64_t kMaxRows = 1 << 26;

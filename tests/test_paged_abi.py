@@ -73,8 +73,12 @@ def test_workspace_sizes(L):
     assert f(128, 1, 128, 8) >= 256 * (1152 + 128 * 512)
     assert f(512, 1, 2 ** 17, 16) < 2 ** 17 * 1152 + 2 ** 32 + 2 ** 20
     # the form that "auto" takes
-    assert f(127, 1, 500, 16) == f(127, 1, 500, 16, "absorbed") != f(127, 1, 500, 16, "expanded")
-    assert f(128, 1, 500, 16) == f(128, 1, 500, 16, "expanded")
+    for n, kv in ((112, 1024), (160, 1025), (160, 4096), (208, 4097)):
+        assert f(n - 1, 1, kv, 16) == f(n - 1, 1, kv, 16, "absorbed")
+        assert f(n, 1, kv, 16) == f(n, 1, kv, 16, "expanded") != f(n, 1, kv, 16, "absorbed")
+    # not the expanded form where it is refused
+    assert f(60000, 200, 2 ** 20, 16) == f(60000, 200, 2 ** 20, 16, "absorbed") > 0
+    assert f(60000, 200, 2 ** 20, 16, "expanded") == 0
     for bad in (dict(form="other"), dict(bits=4)):
         with pytest.raises(L.MLAError):
             f(1, 1, 10, **{"bits": 16, **bad})

@@ -481,6 +481,8 @@ def mla_attend_paged(q_nope: torch.Tensor, q_pe: torch.Tensor, wkv_b: torch.Tens
         raise MLAError("out must be contiguous [N, 128, 128], on the queries' device")
     if N == 0 or S == 0:
         return out
+    if ws is not None and (ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != dev):
+        raise MLAError("ws must be contiguous uint8, on the queries' device")
     pool, kind, P, ps, page, row = _pool(pages)
     with torch.cuda.device(dev):
         if ws is None:

@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(1024) layout_kernel(const Seqs q, const Pool p
                                                        const Layout ly, int classes_shift) {
   __shared__ int part[1024], cls[1024];
   const int tid = threadIdx.x;
+  pdl_trigger();
   const int per = (q.S + 1023) / 1024;
   const int lo = min(q.S, tid * per), hi = min(q.S, lo + per);
   int rows = 0;
@@ -155,6 +156,8 @@ __global__ void __launch_bounds__(256) gather_kernel(const Pool pool, const Layo
                                                       int32_t* __restrict__ table, int max_pages,
                                                       int32_t* status) {
   const int lane = threadIdx.x & 31;
+  pdl_wait();  // the layout
+  pdl_trigger();
   const int total = ld_global_nc_s32_early(ly.row + S);
   for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < total; r += gridDim.x * 8) {
     int a = 0, e = S;  // the last sequence that starts at or before row r
@@ -255,12 +258,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm::THREADS, 1)
   volatile int* abort = &bars.abort;
   const uint32_t rank = cluster_ctarank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // this pair's range of the (256-row block, head) list
-  const long long items =
-      (long long)((ld_global_nc_s32_early(total_rows) + 2 * kRows - 1) / (2 * kRows)) * heads;
-  const int pairs = gridDim.x >> 1, cid = blockIdx.x >> 1;
-  const int lo = (int)(items * cid / pairs), hi = (int)(items * (cid + 1) / pairs);
-
   if (warp == 5) tmem_alloc2(&bars.tmem_base, 512);
   if (tid == 0) {
     for (int i = 0; i < 8; ++i) {
@@ -283,6 +280,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm::THREADS, 1)
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
+  pdl_wait();  // the rows; of a later group, its predecessor's reads of K and V
+  pdl_trigger();
+  // this pair's range of the (256-row block, head) list
+  const long long items =
+      (long long)((ld_global_nc_s32_early(total_rows) + 2 * kRows - 1) / (2 * kRows)) * heads;
+  const int pairs = gridDim.x >> 1, cid = blockIdx.x >> 1;
+  const int lo = (int)(items * cid / pairs), hi = (int)(items * (cid + 1) / pairs);
 
   if (warp == 4) {
     // ---------------- loads: each CTA its own operands ----------------
@@ -513,9 +517,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
   const uint32_t rank = cluster_ctarank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = heads / 2;  // items of a block
-  const int items = ld_global_nc_s32_early(ly.count) * per;
-  const int it0 = blockIdx.x >> 1, step = gridDim.x >> 1;
-
   if (warp == 9) tmem_alloc2(&bars.tmem_base, 512);
   if (tid == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -542,6 +543,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
+  pdl_wait();  // the keys and values
+  pdl_trigger();
+  const int items = ld_global_nc_s32_early(ly.count) * per;
+  const int it0 = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   if (warp == 11) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));  // (idle)
@@ -914,10 +919,10 @@ static int gather_rows(const RowsWs& w, const Pool& pool, const Seqs& q, uint8_t
   const int64_t want = (w.max_rows + 7) / 8;
   const int blocks = (int)(want < sms * 32 ? want : sms * 32);
   if (pool.kind == MLA_PAGE_E4M3)
-    gather_kernel<true><<<blocks, 256, 0, st>>>(pool, ly, q.S, rows, table, max_pages, status);
-  else
-    gather_kernel<false><<<blocks, 256, 0, st>>>(pool, ly, q.S, rows, table, max_pages, status);
-  return launch_status();
+    return launch_pdl(gather_kernel<true>, dim3(blocks), dim3(256), 0, st, pool, ly, q.S, rows,
+                      table, max_pages, status);
+  return launch_pdl(gather_kernel<false>, dim3(blocks), dim3(256), 0, st, pool, ly, q.S, rows,
+                    table, max_pages, status);
 }
 
 static int staged_pages(int max_kv) {
@@ -973,14 +978,15 @@ int run(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const mla_bf16_t* wkv_
   static std::atomic<unsigned long long> gemm_attr{0}, attn_attr{0};
   if (int e = ensure_smem_attr(expand_kernel, gemm::SMEM, &gemm_attr)) return e;
   if (int e = ensure_smem_attr(chunk_kernel, attn::SMEM, &attn_attr)) return e;
+  const dim3 grid(2 * (sms / 2));
   for (int h0 = 0; h0 < kH; h0 += L.heads) {
-    expand_kernel<<<2 * (sms / 2), gemm::THREADS, gemm::SMEM, st>>>(
-        map_c, map_w, map_sk, map_v, ly.row + q.S, h0, L.heads, status);
-    if (int e = launch_status()) return e;
-    chunk_kernel<<<2 * (sms / 2), attn::THREADS, attn::SMEM, st>>>(
-        map_qn, map_qr, map_k, map_r, map_v, ly, h0, L.heads, scale * 1.4426950408889634f,
-        reinterpret_cast<__nv_bfloat16*>(O), status);
-    if (int e = launch_status()) return e;
+    if (int e = launch_pdl(expand_kernel, grid, dim3(gemm::THREADS), gemm::SMEM, st, map_c, map_w,
+                           map_sk, map_v, (const int32_t*)(ly.row + q.S), h0, L.heads, status))
+      return e;
+    if (int e = launch_pdl(chunk_kernel, grid, dim3(attn::THREADS), attn::SMEM, st, map_qn, map_qr,
+                           map_k, map_r, map_v, ly, h0, L.heads, scale * 1.4426950408889634f,
+                           reinterpret_cast<__nv_bfloat16*>(O), status))
+      return e;
   }
   return MLA_OK;
 }

@@ -406,6 +406,8 @@ def test_refusals(shla):
            dict(cu_q=w["cu_q"][:1]), dict(kv_len=w["kv_len"].cpu()), dict(max_kv=0),
            dict(max_kv=2 ** 24 + 1), dict(form="both"), dict(out=w["q_nope"][:1]),
            dict(ws=torch.empty(16, dtype=torch.uint8, device="cuda")),
+           dict(ws=torch.empty(1 << 20, dtype=torch.float32, device="cuda")),
+           dict(ws=torch.empty(1 << 24, dtype=torch.uint8)),
            dict(status=torch.zeros(1, dtype=torch.int32, device="cuda")),
            dict(pages=torch.empty(40 * 577, dtype=torch.bfloat16, device="cuda")[1:].as_strided(
                (2, 16, 576), (16 * 576, 576, 1)))]

@@ -466,30 +466,6 @@ struct Bars {  // "first": waited on by the first CTA; "both": committed to both
   uint32_t tmem_base;
   int abort;
 };
-
-// which of eight pairs of weights are computed without the exponential unit
-constexpr uint32_t kByPolynomial = 0x00;
-
-// 2^x of two x: x = n + f with n the nearest whole number, 2^f by the cubic with
-// the least largest relative error over [-1/2, 1/2] (7.5e-5, found by Remez'
-// exchange; a bf16 rounding of the weight is off by up to 3.9e-3), n added to its
-// exponent.  x below -126 counts as -126.
-DEV void exp2_cubic(float& x, float& y) {
-  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x));
-  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(y));
-  const uint64_t v = pack2(x, y);
-  const uint64_t big = pack2(12582912.f, 12582912.f), nbig = pack2(-12582912.f, -12582912.f);
-  const uint64_t r = add2(v, big);  // n in the low bits
-  const uint64_t f = fma2(add2(r, nbig), pack2(-1.f, -1.f), v);
-  uint64_t p = fma2(f, pack2(0.05517167f, 0.05517167f), pack2(0.24261113f, 0.24261113f));
-  p = fma2(p, f, pack2(0.693260968f, 0.693260968f));
-  p = fma2(p, f, pack2(0.999928057f, 0.999928057f));
-  float rx, ry, px, py;
-  unpack2(r, rx, ry);
-  unpack2(p, px, py);
-  x = u2f(f2u(px) + (f2u(rx) << 23));
-  y = u2f(f2u(py) + (f2u(ry) << 23));
-}
 }  // namespace attn
 
 // D (+)= A B with A in TMEM: each CTA of the pair its own rows at the same address
@@ -744,12 +720,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
 #pragma unroll
         for (int c = 4; c < 124; c += 8)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = max3_nan(mx[e], u2f(s[c + e]), u2f(s[c + 4 + e]));
-        float mt = max3_nan(max3_nan(mx[0], mx[1], mx[2]), u2f(s[124]), u2f(s[125]));
-        mt = max3_nan(max3_nan(mx[3], u2f(s[126]), u2f(s[127])), mt, mt) * scale_log2;
-        // (a score that is not a number, or no finite one, spoils its row for good)
-        if (!(mt < INFINITY)) mt = NAN;
-        const bool raise = !(mt <= m + kRescaleThreshold);
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], u2f(s[c + e]), u2f(s[c + 4 + e]));
+        float mt = max3(max3(mx[0], mx[1], mx[2]), u2f(s[124]), u2f(s[125]));
+        mt = fmaxf(max3(mx[3], u2f(s[126]), u2f(s[127])), mt) * scale_log2;
+        const bool raise = mt > m + kRescaleThreshold;
         if (__any_sync(0xffffffffu, raise)) {
           // (the value products before these scores have completed with them)
           const float a = raise ? fast_exp2(m - mt) : 1.f;  // 0 at the first tile
@@ -780,12 +754,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
             float x, y;
             unpack2(fma2(pack2(u2f(s[2 * (c * 32 + e)]), u2f(s[2 * (c * 32 + e) + 1])), scale2, d2),
                     x, y);
-            if (kByPolynomial >> (e & 7) & 1) {
-              exp2_cubic(x, y);
-            } else {
-              x = fast_exp2(x);
-              y = fast_exp2(y);
-            }
+            x = fast_exp2(x);
+            y = fast_exp2(y);
             if (e & 1) la = add2(la, pack2(x, y));
             else lb = add2(lb, pack2(x, y));
             w2[e] = pack_bf16x2(x, y);

@@ -115,12 +115,6 @@ DEV float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-DEV float max3_nan(float a, float b, float c) {  // NaN if one of them is
-  float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 // 32 lanes x 32 bit, 32 and 16 consecutive columns
 DEV void tmem_ld32(uint32_t taddr, uint32_t* r) {
   asm volatile(

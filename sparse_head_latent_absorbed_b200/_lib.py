@@ -375,8 +375,8 @@ def _pool(pages: torch.Tensor):
     page = pages.stride(0) if P > 1 else ps * row  # (one page: its stride is never used)
     if min(row, page) < 0 or max(row, page) > 2 ** 31 - 1:
         raise MLAError("page strides out of range")
-    size = pages.element_size()
-    return _p(pages), kind, P, ps, page * size, row * size
+    size = 1 if kind else 2
+    return pages.data_ptr(), kind, P, ps, page * size, row * size
 
 
 def _int32(t: torch.Tensor, name: str, dim: int, device) -> torch.Tensor:
@@ -393,7 +393,19 @@ def _status(t: Optional[torch.Tensor], device):
         return None
     if _int32(t, "status", 1, device).numel() < 2:
         raise MLAError("status must be int32 [2]")
-    return _p(t)
+    return t.data_ptr()
+
+
+def _on_device(dev: torch.device, what: str, fn, *args):
+    """fn(*args, stream) with the device's current stream, on the device.  (The
+    raw stream handle, and no guard where the device is current: 4 of the 17 us
+    that a call of a small kernel cost the host.)"""
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, stream), what)
+        return
+    with torch.cuda.device(dev):
+        _check(fn(*args, stream), what)
 
 
 def mla_page_write(rows: torch.Tensor, slots: torch.Tensor, pages: torch.Tensor,
@@ -410,10 +422,9 @@ def mla_page_write(rows: torch.Tensor, slots: torch.Tensor, pages: torch.Tensor,
     if N == 0:
         return
     pool, kind, P, ps, page, row = _pool(pages)
-    with torch.cuda.device(dev):
-        _check(LIB.mla_page_write(_p(rows), rows.stride(0) if N > 1 else 576, _p(slots), N, pool,
-                                  kind, P, ps, page, row, _status(status, dev), _stream(dev)),
-               "mla_page_write")
+    _on_device(dev, "mla_page_write", LIB.mla_page_write, rows.data_ptr(),
+               rows.stride(0) if N > 1 else 576, slots.data_ptr(), N, pool, kind, P, ps, page, row,
+               _status(status, dev))
 
 
 def mla_page_read(pages: torch.Tensor, slots: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -426,14 +437,13 @@ def mla_page_read(pages: torch.Tensor, slots: torch.Tensor, out: Optional[torch.
     if out is None:
         out = torch.empty(N, 576, dtype=torch.bfloat16, device=dev)
     _need(out, torch.bfloat16, "out")
-    if tuple(out.shape) != (N, 576) or out.stride(1) != 1 or out.device != dev:
+    if out.shape != (N, 576) or out.stride(1) != 1 or out.device != dev:
         raise MLAError("out must be [N, 576] with unit inner stride, on the pages' device")
     if N == 0:
         return out
-    with torch.cuda.device(dev):
-        _check(LIB.mla_page_read(pool, kind, P, ps, page, row, _p(slots), N, _p(out),
-                                 out.stride(0) if N > 1 else 576, _status(status, dev),
-                                 _stream(dev)), "mla_page_read")
+    _on_device(dev, "mla_page_read", LIB.mla_page_read, pool, kind, P, ps, page, row,
+               slots.data_ptr(), N, out.data_ptr(), out.stride(0) if N > 1 else 576,
+               _status(status, dev))
     return out
 
 
@@ -484,13 +494,14 @@ def mla_attend_paged(q_nope: torch.Tensor, q_pe: torch.Tensor, wkv_b: torch.Tens
     if ws is not None and (ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != dev):
         raise MLAError("ws must be contiguous uint8, on the queries' device")
     pool, kind, P, ps, page, row = _pool(pages)
-    with torch.cuda.device(dev):
-        if ws is None:
-            ws = torch.empty(mla_attend_paged_workspace_bytes(N, S, max_kv, 8 if kind else 16, form),
-                             dtype=torch.uint8, device=dev)
-        _check(LIB.mla_attend_paged(_p(q_nope), _p(q_pe), _p(wkv_b), pool, kind, P, ps, page, row,
-                                    _p(page_table), page_table.shape[1], _p(cu_q), _p(kv_len), S,
-                                    N, int(max_kv), float(scale), FORMS[form], _p(out), _p(ws),
-                                    ws.numel(), _status(status, dev), _stream(dev)),
-               "mla_attend_paged")
+    if ws is None:
+        # (some sizes depend on the device's SM count)
+        with torch.cuda.device(dev):
+            need = mla_attend_paged_workspace_bytes(N, S, max_kv, 8 if kind else 16, form)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _on_device(dev, "mla_attend_paged", LIB.mla_attend_paged, q_nope.data_ptr(), q_pe.data_ptr(),
+               wkv_b.data_ptr(), pool, kind, P, ps, page, row, page_table.data_ptr(),
+               page_table.shape[1], cu_q.data_ptr(), kv_len.data_ptr(), S, N, int(max_kv),
+               float(scale), FORMS[form], out.data_ptr(), ws.data_ptr(), ws.numel(),
+               _status(status, dev))
     return out

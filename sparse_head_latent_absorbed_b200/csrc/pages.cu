@@ -1,6 +1,8 @@
 // Writing rows into a paged latent cache and reading them back, in 8 or 16
 // bits.  Both are bound by memory: a row is read once and written once
-// (1152 B on the bf16 side, 656 or 1152 B on the page side).
+// (1152 B on the bf16 side, 656 or 1152 B on the page side).  Measured from a cold
+// L2, 8-bit pages: 16384 rows written in 10 us (4.5 at the copy rate), 32768 read
+// in 14 us (9.1); a few rows in 6, which is a launch.
 #include "pages.cuh"
 
 namespace shla {

@@ -342,6 +342,51 @@ def test_captured_call_follows_its_inputs(shla, form):
         assert (out[used:] == 7).all()
 
 
+def test_captured_call_that_converts_its_pages(shla):
+    # as above, of the absorbed form that converts 8-bit pages first; lengths grow
+    # from call to call, and the workspace holds what another call left
+    w = R.make([4, 0, 30], [1500, 900, 1800], 8, 64, 24, pad_tokens=3)
+    N = w["q_nope"].shape[0]
+    full, w["max_kv"] = w["kv_len"].clone(), 9000
+    need = [shla.mla_attend_paged_workspace_bytes(N, 3, 9000, b, "absorbed") for b in (8, 16)]
+    assert need[0] > need[1]
+    ws = torch.empty(need[0], dtype=torch.uint8, device="cuda")
+    out = torch.full_like(w["q_nope"], 7.0)
+    shla.mla_attend_paged(**w, form="absorbed", out=out, ws=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        shla.mla_attend_paged(**w, form="absorbed", out=out, ws=ws)
+    for cut in (1400, 3, 0):
+        w["kv_len"].copy_((full - cut).clamp(min=0))
+        out.fill_(7.0)
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(out[:34], ref_of(w)[:34])
+        assert (out[34:] == 7).all()
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("bits", [16, 8])
+def test_sequences_that_share_pages(shla, form, bits):
+    # a common prefix: the second sequence's first pages are the first one's
+    w = R.make([3, 140, 1], [700, 400, 500], bits, 16, 25)
+    w["page_table"][1, :12] = w["page_table"][0, :12]
+    w["page_table"][2] = w["page_table"][0]
+    check(shla.mla_attend_paged(**w, form=form), ref_of(w))
+
+
+def test_more_positions_than_one_group_of_heads_holds(shla):
+    # the expanded form in groups of 64 heads; checked for six of the 128
+    w = R.make([257, 130], [35000, 34000], 16, 64, 26)
+    got = shla.mla_attend_paged(**w, form="expanded")
+    heads = [0, 1, 63, 64, 65, 127]
+    some = {k: w[k][:, heads] for k in ("q_nope", "q_pe")}
+    want = R.attend(*({**w, **some, "wkv_b": w["wkv_b"][heads]}[k] for k in REF))
+    check(got[:, heads], want)
+
+
 @pytest.mark.parametrize("form", FORMS)
 def test_two_streams_at_once(shla, form):
     ws = [R.make([3, 140], [900, 500], 8, 16, 19), R.make([1, 160], [1200, 400], 16, 64, 20)]

@@ -5,14 +5,16 @@
 //   O[r,h] = softmax_t((q_nope.K + q_pe.kpe) * scale) V.
 // From about 171 new tokens a sequence on this takes fewer flops than folding
 // W_UK into the queries: 81,920 per token and position and head set against
-// 278,528, for 33.6 Mflop a position.  Four kernels:
+// 278,528, for 33.6 Mflop a position.  Five kernels:
 //
 //   layout_kernel   one block: where each sequence's positions go, and the list
-//                   of query blocks (up to 512 tokens), heaviest first
+//                   of query blocks (up to 512 tokens), cut into equal parts
 //   gather_kernel   the pages' rows, as bf16, one sequence after another
 //   expand_kernel   K and V of a group of heads: a GEMM on CTA pairs
-//   chunk_kernel    the attention of the group's heads
-// The last two run once per group; a group is as many heads as the workspace
+//   chunk_kernel    the attention of the group's heads, in one range of equal cost
+//                   for each CTA pair
+//   join_kernel     the outputs of the items that such a range's end cuts
+// The last three run once per group; a group is as many heads as the workspace
 // holds (all 128 up to 65,536 positions).
 #include <math.h>
 
@@ -60,86 +62,122 @@ struct Block {
   }
 };
 
+// Where a pair's work begins: key tile j of item g (item g % (heads / 2) of block
+// g / (heads / 2)).
+struct Cut {
+  int g, j;
+};
+
 struct Layout {
   int32_t* row;    // [S + 1] first gathered row of each sequence (multiples of 128)
   int32_t* kv;     // [S]
   Block* block;    // [N / 256 + S]
-  int32_t* count;  // [1] blocks
+  int32_t* start;  // [N / 256 + S] cost of the blocks before it, for one item of each
+  Cut* cut;        // [pairs + 1]
 };
+
+constexpr int kPairs = 74;    // at most; CTA pairs that share the work
+constexpr int kItemCost = 1;  // of an item, in key tiles: its queries' load and its output
+constexpr int kMinPiece = 4;  // key tiles that a cut leaves on either side
 
 // exclusive prefix sum over the block's 1024 threads; *total: the sum
 DEV int scan1024(int v, int* part, int* total) {
-  const int tid = threadIdx.x;
-  part[tid] = v;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto up = [&](int x) {  // inclusive, over the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  };
+  const int x = up(v);
+  if (lane == 31) part[warp] = x;
   __syncthreads();
-  for (int o = 1; o < 1024; o <<= 1) {
-    const int u = tid >= o ? part[tid - o] : 0;
-    __syncthreads();
-    part[tid] += u;
-    __syncthreads();
-  }
-  const int r = part[tid] - v;
-  *total = part[1023];
+  if (warp == 0) part[32 + lane] = up(part[lane]);
+  __syncthreads();
+  *total = part[63];
+  const int r = (warp ? part[31 + warp] : 0) + x - v;
   __syncthreads();
   return r;
 }
 
-// Blocks are placed by their number of key tiles, most first, in 1024 classes
-// (the order inside a class changes nothing but the order of the work).
+// One block.  Everything follows from the sequences' order alone: where the list
+// is cut decides how some outputs are rounded.
 __global__ void __launch_bounds__(1024) layout_kernel(const Seqs q, const Pool pool,
-                                                       const Layout ly, int classes_shift) {
-  __shared__ int part[1024], cls[1024];
+                                                       const Layout ly, int items, int pairs) {
+  __shared__ int part[64];
   const int tid = threadIdx.x;
   pdl_trigger();
   const int per = (q.S + 1023) / 1024;
   const int lo = min(q.S, tid * per), hi = min(q.S, lo + per);
-  int rows = 0;
+  int rows = 0, blocks = 0;
   for (int s = lo; s < hi; ++s) {
     // a sequence without new tokens needs no keys
-    const int kv = q.q0(s + 1) > q.q0(s) ? q.kv(s, pool) : 0;
+    const int n = q.q0(s + 1) - q.q0(s), kv = n > 0 ? q.kv(s, pool) : 0;
     ly.kv[s] = kv;
     rows += (kv + kRows - 1) / kRows * kRows;
+    blocks += max(0, (n + kTile - 1) / kTile);
   }
-  cls[tid] = 0;
   int total;
   int at = scan1024(rows, part, &total);
-  for (int s = lo; s < hi; ++s) {
-    ly.row[s] = at;
-    at += (ly.kv[s] + kRows - 1) / kRows * kRows;
-  }
   if (tid == 0) ly.row[q.S] = total;
-  auto each = [&](auto f) {
-    for (int s = lo; s < hi; ++s) {
-      const int a = q.q0(s), n = q.q0(s + 1) - a;
-      for (int i = 0; i < n; i += kBlock) {
-        Block b;
-        b.tok = a + i;
-        b.n = min(kBlock, n - i);
-        b.kv = ly.kv[s];
-        b.lim = b.kv - n + i + 1;
-        b.row = ly.row[s];
-        b.upper = 0;
-        const int w = (b.tiles(0) + b.tiles(1)) >> classes_shift;
-        f(b, 1023 - min(1023, w));
-        if (b.two_heads()) continue;
-        b.upper = 1;
-        f(b, 1023 - min(1023, w));
-      }
-    }
-  };
-  each([&](const Block&, int c) { atomicAdd(&cls[c], 1); });
-  __syncthreads();
-  const int mine = cls[tid];
-  const int first = scan1024(mine, part, &total);
-  cls[tid] = first;
   // (ranges of a cu_q that decreases may overlap: no more blocks than there is room for)
   const int room = q.N / kTile + q.S;
-  if (tid == 0) *ly.count = min(total, room);
+  int i = min(scan1024(blocks, part, &total), room);
+  const int first = i, n = min(total, room);
+  int cost = 0;
+  for (int s = lo; s < hi; ++s) {
+    ly.row[s] = at;
+    const int t0 = q.q0(s), len = q.q0(s + 1) - t0;
+    for (int k = 0; k < len && i < room; k += kBlock) {
+      Block b;
+      b.tok = t0 + k;
+      b.n = min(kBlock, len - k);
+      b.kv = ly.kv[s];
+      b.lim = b.kv - len + k + 1;
+      b.row = at;
+      b.upper = 0;
+      const int c = b.tiles(1) + kItemCost;
+      ly.block[i++] = b;
+      cost += c;
+      if (b.two_heads() || i >= room) continue;
+      b.upper = 1;
+      ly.block[i++] = b;
+      cost += c;
+    }
+    at += (ly.kv[s] + kRows - 1) / kRows * kRows;
+  }
+  // the list cut into one range of equal cost for each pair
+  int all;
+  int run = scan1024(cost, part, &all);
+  for (int k = first; k < i; ++k) {
+    ly.start[k] = run;
+    run += ly.block[k].tiles(1) + kItemCost;
+  }
   __syncthreads();
-  each([&](const Block& b, int c) {
-    const int i = atomicAdd(&cls[c], 1);
-    if (i < room) ly.block[i] = b;
-  });
+  if (tid <= pairs) {
+    Cut c = {n * items, 0};
+    if (tid < pairs && n > 0) {
+      const long long u = (long long)tid * all * items / pairs;
+      int a = 0, e = n;  // start[a] * items <= u
+      while (e - a > 1) {
+        const int m = (a + e) >> 1;
+        if ((long long)ly.start[m] * items <= u) a = m; else e = m;
+      }
+      const int tiles = ly.block[a].tiles(1), one = tiles + kItemCost;
+      const long long in = u - (long long)ly.start[a] * items;
+      c.g = a * items + (int)(in / one);
+      c.j = (int)(in % one) - kItemCost;
+      if (c.j < kMinPiece) {
+        c.j = 0;
+      } else if (tiles - c.j < kMinPiece) {
+        c.j = 0;
+        ++c.g;
+      }
+    }
+    ly.cut[tid] = c;
+  }
 }
 
 // ===========================================================================
@@ -440,10 +478,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm::THREADS, 1)
 // the first half of the keys' weights is multiplied while the second half is
 // still being computed.  P overlays its scores, rounded to bf16 as a tensor-core
 // operand (the row sum is of the fp32 weights).
-// Measured: 512 tokens over 6000 positions, 128 heads, 215 us (1.12 PFLOP/s).  What
-// bounds it is a tile's chain: 1480 cycles of softmax (1024 of them its 128
+// The list of items (a block and a head or two) is cut into one range of equal
+// cost for each pair; what a cut leaves is joined by the next kernel.  (Whole items
+// dealt out in turn: 128 for 74 pairs take two turns, 14% of the time idle.)
+// Measured: 512 tokens over 6000 positions, 128 heads, 195 us (1.24 PFLOP/s); over
+// 50000, 1980 us at 1.55 to 1.6 GHz, where the power limit holds the clock.  What
+// bounds the cycles is a tile's chain: 1480 of softmax (1024 of them its 128
 // exponentials a thread), about 400 until both CTAs' weights are known to the
-// issuer, then its own products while the other tile's wait; two tiles take 3450
+// issuer, then its own products while the other tile's wait; two tiles take 3350
 // cycles, their products 2580.  TMEM has no room for a third.
 // Warps 0-3 and 4-7: softmax and output of tile 0 and 1; warp 8: queries and
 // keys by TMA; warp 9: MMA (of the pair's first CTA); warp 10: values by TMA.
@@ -474,6 +516,43 @@ struct Bars {  // "first": waited on by the first CTA; "both": committed to both
   uint32_t tmem_base;
   int abort;
 };
+
+// A pair's work: items, or parts of the key tiles of its first and last.
+struct Work {
+  Block b;
+  int i, j0, j1;  // item, key tiles [j0, j1)
+  DEV bool whole() const { return j0 == 0 && j1 == b.tiles(1); }
+  DEV int count(int t) const { return max(0, min(j1, b.tiles(t)) - j0); }  // of query tile t
+};
+struct Range {
+  int g, j, ge, je;
+  DEV Range(const Cut* cut, int pair) {
+    g = cut[pair].g;
+    j = cut[pair].j;
+    ge = cut[pair + 1].g;
+    je = cut[pair + 1].j;
+  }
+  DEV bool next(const Layout& ly, int per, Work* w) {
+    if (g > ge || (g == ge && j >= je)) return false;
+    w->b = ly.block[g / per];
+    w->i = g % per;
+    w->j0 = j;
+    w->j1 = g == ge ? je : w->b.tiles(1);
+    ++g;
+    j = 0;
+    return true;
+  }
+};
+
+// What a pair leaves of an item that others work on too: by slot (0: the pair's
+// first piece, of which it does not have the beginning; 1: its last), query
+// tile and CTA, 128 rows of the normalised output and the log2 of the sum of
+// exponentials.
+constexpr int SLOT_ROWS = 4 * kRows;
+struct Parts {
+  __nv_bfloat16* o;  // [pairs][2][2][2][128][128]
+  float* lse;        // [pairs][2][2][2][128]
+};
 }  // namespace attn
 
 // D (+)= A B with A in TMEM: each CTA of the pair its own rows at the same address
@@ -490,8 +569,9 @@ DEV void tc_mma2_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_constant__ CUtensorMap map_qr,
                  const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_r,
-                 const __grid_constant__ CUtensorMap map_v, const Layout ly, int head0, int heads,
-                 float scale_log2, __nv_bfloat16* __restrict__ O, int32_t* status) {
+                 const __grid_constant__ CUtensorMap map_v, const Layout ly,
+                 const attn::Parts parts, int head0, int heads, float scale_log2,
+                 __nv_bfloat16* __restrict__ O, int32_t* status) {
   using namespace attn;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = paged::align1024(smem_raw);
@@ -529,8 +609,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
   const uint32_t tmem = bars.tmem_base;
   pdl_wait();  // the keys and values
   pdl_trigger();
-  const int items = ld_global_nc_s32_early(ly.count) * per;
-  const int it0 = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int pair = blockIdx.x >> 1;
+  Range range(ly.cut, pair);
+  Work w;
 
   if (warp == 11) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));  // (idle)
@@ -541,18 +622,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
     const uint32_t k_full0 = mapa_shared(smem_u32(&bars.k_full[0]), 0);
     int u = 0, qn[2] = {0, 0};
     bool ok = true;
-    for (int it = it0; it < items && ok; it += step) {
-      const Block b = ly.block[it / per];
-      const int nt[2] = {b.tiles(0), b.tiles(1)};
+    while (ok && range.next(ly, per, &w)) {
+      const Block& b = w.b;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        if (nt[t] == 0) continue;
+        if (w.count(t) == 0) continue;
         ok = ok && warp_wait(&bars.q_free[t], (qn[t] & 1) ^ 1, abort, status);
         if (!ok) break;
         if (lane == 0) {
           if (rank == 0) mbar_arrive_expect_tx(&bars.q_full[t], 2 * Q_BYTES);
           const uint32_t dst = sbase + t * Q_BYTES, bar = q_full0 + t * 8;
-          const int h = head0 + b.head(t, it % per, heads);
+          const int h = head0 + b.head(t, w.i, heads);
           const int tok = b.tok + b.first(t) + rank * b.width();
           tma_load_3d_pair(dst, &map_qn, 0, h, tok, bar);
           tma_load_3d_pair(dst + Q_BYTES / 3, &map_qn, 64, h, tok, bar);
@@ -561,7 +641,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
         ++qn[t];
       }
       const int two = b.two_heads();
-      for (int j = 0; j < nt[1] && ok; ++j)
+      for (int j = w.j0; j < w.j1 && ok; ++j)
         for (int t = two ? 0 : 1; t < 2; ++t) {
           const int s = u % NK;
           ok = ok && warp_wait(&bars.k_empty[s], ((u / NK) & 1) ^ 1, abort, status);
@@ -570,7 +650,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
             if (rank == 0) mbar_arrive_expect_tx(&bars.k_full[s], 2 * K_BYTES);
             const uint32_t dst = sbase + OFF_K + s * K_BYTES;
             const int r = b.row + j * kRows + rank * 64;
-            tma_load_3d_pair(dst, &map_k, 0, r, 2 * b.head(t, it % per, heads), k_full0 + s * 8);
+            tma_load_3d_pair(dst, &map_k, 0, r, 2 * b.head(t, w.i, heads), k_full0 + s * 8);
             tma_load_2d_pair(dst + K_BYTES / 3 * 2, &map_r, 0, r, k_full0 + s * 8);
           }
           ++u;
@@ -583,10 +663,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
     const uint32_t v_full0 = mapa_shared(smem_u32(&bars.v_full[0]), 0);
     int u = 0;
     bool ok = true;
-    for (int it = it0; it < items && ok; it += step) {
-      const Block b = ly.block[it / per];
-      const int n = b.tiles(1), two = b.two_heads();
-      for (int j = 0; j < n && ok; ++j)
+    while (ok && range.next(ly, per, &w)) {
+      const Block& b = w.b;
+      const int two = b.two_heads();
+      for (int j = w.j0; j < w.j1 && ok; ++j)
         for (int t = two ? 0 : 1; t < 2; ++t) {
           const int s = u % NV;
           ok = ok && warp_wait(&bars.v_empty[s], ((u / NV) & 1) ^ 1, abort, status);
@@ -594,7 +674,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
           if (lane == 0) {
             if (rank == 0) mbar_arrive_expect_tx(&bars.v_full[s], 2 * V_BYTES);
             tma_load_3d_pair(sbase + OFF_V + s * V_BYTES, &map_v, 0, b.row + j * kRows,
-                             2 * b.head(t, it % per, heads) + rank, v_full0 + s * 8);
+                             2 * b.head(t, w.i, heads) + rank, v_full0 + s * 8);
           }
           ++u;
         }
@@ -662,10 +742,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
         }
         __syncwarp();
       };
-      for (int it = it0; it < items && ok; it += step) {
-        const Block b = ly.block[it / per];
-        const int nt[2] = {b.tiles(0), b.tiles(1)};  // nt[0] <= nt[1]
-        const bool two = b.two_heads();
+      while (ok && range.next(ly, per, &w)) {
+        const int nt[2] = {w.count(0), w.count(1)};  // nt[0] <= nt[1]
+        const bool two = w.b.two_heads();
         const int per_j = two ? 2 : 1;
         auto at = [&](int t, int j) { return u0 + j * per_j + (two ? t : 0); };
 #pragma unroll
@@ -699,43 +778,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
     int sn = 0, on = 0;
     bool ok = true;
     const uint64_t scale2 = pack2(scale_log2, scale_log2);
-    for (int it = it0; it < items && ok; it += step) {
-      const Block b = ly.block[it / per];
-      const int nt = b.tiles(t), w = b.width();
-      const int tok0 = b.first(t) + rank * w;  // this CTA's first token of the tile, in the block
-      const int mine = min(min(b.n, b.first(t) + 2 * w) - tok0, w);
+    while (ok && range.next(ly, per, &w)) {
+      const Block& b = w.b;
+      const int nt = w.count(t), width = b.width();
+      const int tok0 = b.first(t) + rank * width;  // this CTA's first token of the tile, in the block
+      const int mine = min(min(b.n, b.first(t) + 2 * width) - tok0, width);
       const int lim0 = b.lim + tok0;            // positions that one sees
       const int lim = min(b.kv, lim0 + row);    // ... this thread's
       float m = -INFINITY;
       uint64_t la = 0, lb = 0;  // partial row sums
 #pragma unroll 1
-      for (int j = 0; j < nt; ++j) {
+      for (int j = w.j0; j < w.j0 + nt; ++j) {
         ok = warp_wait(&bars.s_full[t], sn & 1, abort, status);
         ++sn;
         if (!ok) break;
         tc_fence_after();
-        uint32_t s[128];
+        // (the scores are read again for their weights, in a loop: unrolled over the
+        // tile the code of all roles would not stay in the instruction cache)
+        float mt;
+        {
+          uint32_t s[128];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, s + c * 32);
-        tc_wait_ld();
-        if (min(b.kv, lim0) < (j + 1) * kRows) {
-          const int left = lim - j * kRows;
+          for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, s + c * 32);
+          tc_wait_ld();
+          if (min(b.kv, lim0) < (j + 1) * kRows) {
+            const int left = lim - j * kRows;
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= left) s[c] = 0xff800000u;
+            for (int c = 0; c < 128; ++c)
+              if (c >= left) s[c] = 0xff800000u;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              tmem_st32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(s + c * 32));
+            tc_wait_st();
+          }
+          float mx[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mx[e] = fmaxf(u2f(s[e]), u2f(s[8 + e]));
+#pragma unroll
+          for (int c = 16; c < 128; c += 16)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mx[e] = max3(mx[e], u2f(s[c + e]), u2f(s[c + 8 + e]));
+          mt = fmaxf(max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), mx[6]), mx[7]) * scale_log2;
         }
-        float mx[4] = {u2f(s[0]), u2f(s[1]), u2f(s[2]), u2f(s[3])};
-#pragma unroll
-        for (int c = 4; c < 124; c += 8)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], u2f(s[c + e]), u2f(s[c + 4 + e]));
-        float mt = max3(max3(mx[0], mx[1], mx[2]), u2f(s[124]), u2f(s[125]));
-        mt = fmaxf(max3(mx[3], u2f(s[126]), u2f(s[127])), mt) * scale_log2;
         const bool raise = mt > m + kRescaleThreshold;
         if (__any_sync(0xffffffffu, raise)) {
           // (the value products before these scores have completed with them)
           const float a = raise ? fast_exp2(m - mt) : 1.f;  // 0 at the first tile
-          if (j > 0) {
+          if (j > w.j0) {
 #pragma unroll 1
             for (int c = 0; c < 128; c += 32) {
               uint32_t o[32];
@@ -754,25 +843,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
         // (a token that has seen no position yet has m = -inf: its weights are exp2(-inf) = 0)
         const float d = m == -INFINITY ? 0.f : -m;
         const uint64_t d2 = pack2(d, d);
+        auto weights = [&](const uint32_t* s, int c) {
+          uint32_t w2[16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t w2[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
+          for (int e = 0; e < 16; ++e) {
             float x, y;
-            unpack2(fma2(pack2(u2f(s[2 * (c * 32 + e)]), u2f(s[2 * (c * 32 + e) + 1])), scale2, d2),
-                    x, y);
+            unpack2(fma2(pack2(u2f(s[2 * e]), u2f(s[2 * e + 1])), scale2, d2), x, y);
             x = fast_exp2(x);
             y = fast_exp2(y);
             if (e & 1) la = add2(la, pack2(x, y));
             else lb = add2(lb, pack2(x, y));
             w2[e] = pack_bf16x2(x, y);
           }
-          tmem_st32(ts + c * 32, w2);
+          tmem_st16(ts + c * 16, w2);
+        };
+        uint32_t s0[32], s1[32];
+        tmem_ld32(ts, s0);
+        tc_wait_ld();
+#pragma unroll 1
+        for (int c = 0; c < 4; c += 2) {
+          tmem_ld32(ts + (c + 1) * 32, s1);
+          weights(s0, c);
+          tc_wait_ld();
+          tmem_ld32(ts + ((c + 2) & 3) * 32, s0);
+          weights(s1, c + 1);
+          tc_wait_ld();
           tc_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_pair(p_full0 + c * 8);
+          if (lane == 0) mbar_arrive_pair(p_full0 + (c >> 1) * 8);
         }
       }
       if (!ok) break;
@@ -787,8 +886,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
         if (!ok) break;
         tc_fence_after();
       }
-      __nv_bfloat16* dst = O + ((size_t)(b.tok + tok0 + row) * kH + head0 +
-                                b.head(t, it % per, heads)) * kD;
+      __nv_bfloat16* dst;
+      bool store = row < mine;
+      if (w.whole()) {
+        dst = O + ((size_t)(b.tok + tok0 + row) * kH + head0 + b.head(t, w.i, heads)) * kD;
+      } else {
+        const size_t at = (size_t)(pair * 2 + (w.j0 > 0 ? 0 : 1)) * SLOT_ROWS +
+                          (t * 2 + rank) * kRows + row;
+        float x, y;
+        unpack2(add2(la, lb), x, y);
+        const float l = nt > 0 ? x + y : 0.f;
+        parts.lse[at] = l == 0.f ? -INFINITY : m + log2f(l);
+        dst = parts.o + at * kD;
+        store = store && nt > 0;
+      }
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         uint32_t o[32];
@@ -796,7 +907,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
           tmem_ld32(to + c, o);
           tc_wait_ld();
         }
-        if (row < mine) {
+        if (store) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint4 v = make_uint4(0, 0, 0, 0);
@@ -830,12 +941,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
 }
 
 // ===========================================================================
+// join_kernel: the outputs of the items that several pairs worked on,
+//   O = sum_s 2^(lse_s - max) O_s / sum_s 2^(lse_s - max)
+// Grid (pairs - 1 boundaries, query tile and CTA, four groups of 32 rows); a
+// boundary that cuts no item, or one that an earlier boundary cuts too, has
+// nothing to do.  256 threads: a row's sixteen 16-byte pieces.
+// ===========================================================================
+__global__ void __launch_bounds__(256) join_kernel(const Layout ly, const attn::Parts parts,
+                                                    int pairs, int head0, int heads,
+                                                    __nv_bfloat16* __restrict__ O) {
+  using namespace attn;
+  // every block waits: the kernel after this one relies on it
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x + 1, t = blockIdx.y >> 1, rank = blockIdx.y & 1;
+  const Cut cut = ly.cut[c], before = ly.cut[c - 1];
+  if (cut.j == 0 || (before.g == cut.g && before.j > 0)) return;
+  int last = c;  // the pair that holds the item's last piece
+  while (last + 1 < pairs && ly.cut[last + 1].g == cut.g && ly.cut[last + 1].j > 0) ++last;
+  const int per = heads / 2;
+  const Block b = ly.block[cut.g / per];
+  const int w = b.width(), tok0 = b.first(t) + rank * w;
+  const int mine = min(min(b.n, b.first(t) + 2 * w) - tok0, w);
+  const int head = head0 + b.head(t, cut.g % per, heads);
+  auto at = [&](int s, int row) {  // piece s: the first is its pair's last, the others their pairs' first
+    return (size_t)(s < c ? (c - 1) * 2 + 1 : s * 2) * SLOT_ROWS + (t * 2 + rank) * kRows + row;
+  };
+  const int chunk = threadIdx.x & 15;
+  for (int row = blockIdx.z * 32 + (threadIdx.x >> 4); row < min(mine, (int)blockIdx.z * 32 + 32);
+       row += 16) {
+    float top = -INFINITY;
+    for (int s = c - 1; s <= last; ++s) top = fmaxf(top, parts.lse[at(s, row)]);
+    float sum = 0.f, acc[8] = {};
+    for (int s = c - 1; s <= last; ++s) {
+      const float lse = parts.lse[at(s, row)];
+      if (lse == -INFINITY) continue;  // (its output is not written)
+      const float f = exp2f(lse - top);
+      const uint4 v = *reinterpret_cast<const uint4*>(parts.o + at(s, row) * kD + chunk * 8);
+      const uint32_t p[4] = {v.x, v.y, v.z, v.w};
+      sum += f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[2 * e] += f * u2f(p[e] << 16);
+        acc[2 * e + 1] += f * u2f(p[e] & 0xffff0000u);
+      }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : sum;  // (0: the token sees nothing; NaN stays)
+    uint4 v = make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                         pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+    *reinterpret_cast<uint4*>(O + ((size_t)(b.tok + tok0 + row) * kH + head) * kD + chunk * 8) = v;
+  }
+}
+
+// ===========================================================================
 // host
 // ===========================================================================
 
 // The first part of a workspace: the layout and the gathered rows.
 struct RowsWs {
-  size_t row, kv, block, count, rows, total;
+  size_t row, kv, block, start, cut, rows, total;
   int64_t max_rows;
 };
 
@@ -847,15 +1011,16 @@ static RowsWs rows_ws(int N, int S, int max_kv) {
   w.row = 0;
   w.kv = round_up((size_t)(S + 1) * 4, 256);
   w.block = round_up(w.kv + (size_t)S * 4, 256);
-  w.count = round_up(w.block + ((size_t)N / kTile + S) * sizeof(Block), 256);
-  w.rows = w.count + 256;
+  w.start = round_up(w.block + ((size_t)N / kTile + S) * sizeof(Block), 256);
+  w.cut = round_up(w.start + ((size_t)N / kTile + S) * 4, 256);
+  w.rows = round_up(w.cut + (kPairs + 1) * sizeof(Cut), 256);
   w.total = round_up(w.rows + (size_t)w.max_rows * MLA_ROW * 2, 256);
   return w;
 }
 
 struct Ws {
   RowsWs r;
-  size_t k, v, total;
+  size_t k, v, parts, lse, total;
   int heads;  // of a group
 };
 
@@ -866,7 +1031,9 @@ static Ws layout(int N, int S, int max_kv) {
   while (w.heads > 8 && (size_t)w.r.max_rows * w.heads * 2 * kD * 2 > kGroupBytes) w.heads /= 2;
   w.k = w.r.total;
   w.v = w.k + (size_t)w.r.max_rows * w.heads * kD * 2;
-  w.total = w.v + (size_t)w.r.max_rows * w.heads * kD * 2;
+  w.parts = w.v + (size_t)w.r.max_rows * w.heads * kD * 2;
+  w.lse = w.parts + (size_t)kPairs * 2 * attn::SLOT_ROWS * kD * 2;
+  w.total = w.lse + (size_t)kPairs * 2 * attn::SLOT_ROWS * 4;
   return w;
 }
 
@@ -881,18 +1048,20 @@ static Layout make_layout(const RowsWs& w, uint8_t* ws) {
   ly.row = reinterpret_cast<int32_t*>(ws + w.row);
   ly.kv = reinterpret_cast<int32_t*>(ws + w.kv);
   ly.block = reinterpret_cast<Block*>(ws + w.block);
-  ly.count = reinterpret_cast<int32_t*>(ws + w.count);
+  ly.start = reinterpret_cast<int32_t*>(ws + w.start);
+  ly.cut = reinterpret_cast<Cut*>(ws + w.cut);
   return ly;
 }
 
+static int pairs_of(int sms) { return sms / 2 < kPairs ? sms / 2 : kPairs; }
+
 // layout_kernel and gather_kernel
 static int gather_rows(const RowsWs& w, const Pool& pool, const Seqs& q, uint8_t* ws,
-                       int32_t* table, int max_pages, int sms, int32_t* status, cudaStream_t st) {
+                       int32_t* table, int max_pages, int heads, int sms, int32_t* status,
+                       cudaStream_t st) {
   const Layout ly = make_layout(w, ws);
   __nv_bfloat16* rows = reinterpret_cast<__nv_bfloat16*>(ws + w.rows);
-  int shift = 0;  // key tiles of a query block into 1024 classes
-  while ((2 * ((q.max_kv + kRows - 1) / kRows) >> shift) > 1023) ++shift;
-  layout_kernel<<<1, 1024, 0, st>>>(q, pool, ly, shift);
+  layout_kernel<<<1, 1024, 0, st>>>(q, pool, ly, heads / 2, pairs_of(sms));
   if (int e = launch_status()) return e;
   const int64_t want = (w.max_rows + 7) / 8;
   const int blocks = (int)(want < sms * 32 ? want : sms * 32);
@@ -926,7 +1095,7 @@ int stage(const Pool& pool, const Seqs& q, uint8_t* ws, int32_t* status, cudaStr
   staged->table = table;
   staged->max_pages = staged_pages(q.max_kv);
   paged::set_division(staged);
-  return gather_rows(w, pool, q, ws, table, staged->max_pages, sms, status, st);
+  return gather_rows(w, pool, q, ws, table, staged->max_pages, 2, sms, status, st);
 }
 
 int run(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const mla_bf16_t* wkv_b,
@@ -935,7 +1104,7 @@ int run(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const mla_bf16_t* wkv_
   const Ws L = layout(q.N, q.S, q.max_kv);
   int sms = 0;
   if (int e = check_device(&sms)) return e;
-  if (int e = gather_rows(L.r, pool, q, ws, nullptr, 0, sms, status, st)) return e;
+  if (int e = gather_rows(L.r, pool, q, ws, nullptr, 0, L.heads, sms, status, st)) return e;
   const Layout ly = make_layout(L.r, ws);
   __nv_bfloat16* rows = reinterpret_cast<__nv_bfloat16*>(ws + L.r.rows);
   __nv_bfloat16* k = reinterpret_cast<__nv_bfloat16*>(ws + L.k);
@@ -957,14 +1126,23 @@ int run(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const mla_bf16_t* wkv_
   if (int e = ensure_smem_attr(expand_kernel, gemm::SMEM, &gemm_attr)) return e;
   if (int e = ensure_smem_attr(chunk_kernel, attn::SMEM, &attn_attr)) return e;
   const dim3 grid(2 * (sms / 2));
+  const int pairs = pairs_of(sms);
+  const attn::Parts parts = {reinterpret_cast<__nv_bfloat16*>(ws + L.parts),
+                             reinterpret_cast<float*>(ws + L.lse)};
+  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(O);
   for (int h0 = 0; h0 < kH; h0 += L.heads) {
     if (int e = launch_pdl(expand_kernel, grid, dim3(gemm::THREADS), gemm::SMEM, st, map_c, map_w,
                            map_sk, map_v, (const int32_t*)(ly.row + q.S), h0, L.heads, status))
       return e;
-    if (int e = launch_pdl(chunk_kernel, grid, dim3(attn::THREADS), attn::SMEM, st, map_qn, map_qr,
-                           map_k, map_r, map_v, ly, h0, L.heads, scale * 1.4426950408889634f,
-                           reinterpret_cast<__nv_bfloat16*>(O), status))
+    if (int e = launch_pdl(chunk_kernel, dim3(2 * pairs), dim3(attn::THREADS), attn::SMEM, st,
+                           map_qn, map_qr, map_k, map_r, map_v, ly, parts, h0, L.heads,
+                           scale * 1.4426950408889634f, out, status))
       return e;
+    // (no item is cut that has fewer key tiles than two pieces)
+    if (q.max_kv > (2 * kMinPiece - 1) * kRows && pairs > 1)
+      if (int e = launch_pdl(join_kernel, dim3(pairs - 1, 4, 4), dim3(256), 0, st, ly, parts, pairs,
+                             h0, L.heads, out))
+        return e;
   }
   return MLA_OK;
 }

@@ -9,8 +9,8 @@ value, so by 2^-8 / sqrt(3) = 2.3e-3 in the mean square at worst.  The absorbed
 form rounds q~ (a relative error of the scores, which have a spread of about 1,
 so the same relative error of the weights), the weights, the mixed latent (a
 split token's twice) and the output: sqrt(5) * 2.3e-3 = 5.0e-3 of the output's
-norm.  The expanded form rounds keys, weights, values and output, sqrt(4) of
-them.  REL allows twice that.  One element's error is a sum of many, so close to
+norm.  The expanded form rounds keys, weights, values, output and, where work
+is split, partial outputs: as many.  REL allows twice that.  One element's error is a sum of many, so close to
 normal with 5e-3 of its row's mean square as deviation: over 10^6 elements 6
 deviations, 3e-2, plus its own rounding; ELEM allows 4e-2.  Where a scale
 factor f > 1 widens the scores' spread to f, q~'s share grows f-fold.

@@ -71,7 +71,7 @@ def test_workspace_sizes(L):
     assert own == f(16, 5, 16384, 16, "absorbed") == f(16, 5, 1 << 20, 8, "absorbed")
     # keys and values of 128 heads, of fewer where they would pass 4 GiB
     assert f(128, 1, 128, 8) >= 256 * (1152 + 128 * 512)
-    assert f(512, 1, 2 ** 17, 16) < 2 ** 17 * 1152 + 2 ** 32 + 2 ** 20
+    assert f(512, 1, 2 ** 17, 16) < 2 ** 17 * 1152 + 2 ** 32 + 21 * 2 ** 20
     # the form that "auto" takes
     for n, kv in ((112, 1024), (160, 1025), (160, 4096), (208, 4097)):
         assert f(n - 1, 1, kv, 16) == f(n - 1, 1, kv, 16, "absorbed")

@@ -471,7 +471,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm::THREADS, 1)
 // of a key tile, 64 columns of a value tile.  One CTA alone (M = 128) reads 8 KB
 // of operands for the 64 cycles of a score product, all that shared memory gives;
 // then every wait and every load held up the products: 2060 cycles a tile instead
-// of the 1290 that they take, 2590 us for 512 tokens over 50000 positions against
+// of the 1290 that they take, 2590 us for 1024 tokens over 32768 positions against
 // the pair's 2180 (which reads 6 KB).
 // One fp32 online softmax per token, a thread each: no shuffles.  While one
 // query tile's scores are in the softmax the tensor cores work for the other;
@@ -481,8 +481,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm::THREADS, 1)
 // The list of items (a block and a head or two) is cut into one range of equal
 // cost for each pair; what a cut leaves is joined by the next kernel.  (Whole items
 // dealt out in turn: 128 for 74 pairs take two turns, 14% of the time idle.)
-// Measured: 512 tokens over 6000 positions, 128 heads, 195 us (1.24 PFLOP/s); over
-// 50000, 1980 us at 1.55 to 1.6 GHz, where the power limit holds the clock.  What
+// Measured: 512 tokens over 6000 positions, 128 heads, 195 us (1.24 PFLOP/s); 1024
+// over 32768, 1980 us at 1.55 to 1.6 GHz, where the power limit holds the clock.  What
 // bounds the cycles is a tile's chain: 1480 of softmax (1024 of them its 128
 // exponentials a thread), about 400 until both CTAs' weights are known to the
 // issuer, then its own products while the other tile's wait; two tiles take 3350

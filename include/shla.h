@@ -454,9 +454,9 @@ int mla_page_read(const void* pool, int kind, int num_pages, int page_size, int6
  *   status     optional int32[2].  An entry of page_table outside [0, num_pages)
  *              for a page below a sequence's length reads as a page of zeros
  *              and is counted once in status[1].
- * Cached values at positions below kv_len[s] are taken to be finite: a NaN or
- * infinity there makes the tokens that see it NaN and may do so to earlier
- * tokens of the same call.  What the pages hold from kv_len[s] on does not
+ * Cached values at positions below kv_len[s] are taken to be finite: a NaN
+ * there makes the tokens that see it NaN, an infinity may, and both may do so to
+ * earlier tokens of the same sequence in the call.  What the pages hold from kv_len[s] on does not
  * matter.
  * 1 <= N <= 65535, 1 <= S <= 65535, 1 <= max_kv <= 2^24; absorbed: N *
  * ceil(max_kv / 128) < 2^30; expanded: S * max_kv, each length rounded up to

@@ -388,6 +388,26 @@ def test_more_positions_than_one_group_of_heads_holds(shla):
 
 
 @pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("column", [5, 500, 560])
+def test_nan_stays_with_the_tokens_that_see_it(shla, form, bits, column):
+    # in a latent or a rotary value of position 1037 of the first sequence, which
+    # all its new tokens see; the others keep their results
+    w = R.make([2, 130, 1], [1500, 260, 70], bits, 16, 27)
+    good = shla.mla_attend_paged(**w, form=form)
+    page, o = int(w["page_table"][0, 1037 // 16]), 1037 % 16
+    if bits == 16:
+        w["pages"][page, o, column] = float("nan")
+    elif column < 512:
+        w["pages"][page, o, 512:528].view(torch.float32)[column // 128] = float("nan")
+    else:
+        w["pages"][page, o, 528:].view(torch.bfloat16)[column - 512] = float("nan")
+    got = shla.mla_attend_paged(**w, form=form)
+    assert torch.isnan(got[:2]).all()
+    assert torch.equal(got[2:], good[2:])
+
+
+@pytest.mark.parametrize("form", FORMS)
 def test_two_streams_at_once(shla, form):
     ws = [R.make([3, 140], [900, 500], 8, 16, 19), R.make([1, 160], [1200, 400], 16, 64, 20)]
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]

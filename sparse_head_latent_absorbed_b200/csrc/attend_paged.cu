@@ -158,9 +158,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Seqs q, const Pool poo
 // the next tile's first chunk lands while this tile's last is in use, so the
 // reload waits neither for the softmax nor for the rest of the tile.
 // Measured: 64 sequences of 1000 to 8000 positions, 16-bit pages, one token each:
-// 88 us for 348 MB (4.0 TB/s; 52% of the tensor pipe's cycles), about 3000 cycles a
-// tile; the rest is what a tile's chain from scores to weights to values leaves
-// idle between the two groups.  8-bit pages, 128 sequences up to 16000: 460 us, 31%.
+// 83 us for 348 MB (4.2 TB/s; half of the tensor pipe's cycles), about 2800 cycles
+// a tile; the rest is what a tile's chain from scores to weights to values, and the
+// reload of its keys, leave idle.  8-bit pages, 128 sequences up to 16000: 441 us.
 // There a tile's place in shared memory is filled by the converting warps, and
 // waiting for the place, loading, converting (50 of 280 us, with four tokens each),
 // storing (40) and the softmax add up; tiles of 64 keys with two places took longer.

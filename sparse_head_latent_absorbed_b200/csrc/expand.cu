@@ -818,7 +818,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
           for (int c = 16; c < 128; c += 16)
 #pragma unroll
             for (int e = 0; e < 8; ++e) mx[e] = max3(mx[e], u2f(s[c + e]), u2f(s[c + 8 + e]));
-          mt = fmaxf(max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), mx[6]), mx[7]) * scale_log2;
+          mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) *
+               scale_log2;
         }
         const bool raise = mt > m + kRescaleThreshold;
         if (__any_sync(0xffffffffu, raise)) {
@@ -865,7 +866,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
           tmem_ld32(ts + (c + 1) * 32, s1);
           weights(s0, c);
           tc_wait_ld();
-          tmem_ld32(ts + ((c + 2) & 3) * 32, s0);
+          if (c == 0) tmem_ld32(ts + 64, s0);
           weights(s1, c + 1);
           tc_wait_ld();
           tc_wait_st();

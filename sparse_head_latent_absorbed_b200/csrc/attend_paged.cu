@@ -921,119 +921,176 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::thread
 
 // ===========================================================================
 // merge: O~ = sum_s 2^(lse_s - max) O~_s / sum_s 2^(lse_s - max) over the
-// segments of the tokens that several pairs held (the plan's list).  A unit of
-// work is a token and eight heads, or two when few tokens are split (then each
-// has many segments); 256 threads: a head's 64 16-byte chunks, four threads
-// for each chunk's segments (or four heads at once).  Bound by latency: three
-// dependent loads before the partial outputs, 2 x 1 KB a head and segment.
-// (A block for each boundary and head, most of them with nothing to do, took
-// 25 us where this takes 6.)
+// segments of the tokens that several pairs held (the plan's list).  Many split
+// tokens: a warp for each token and head (or a few heads of it), without a barrier,
+// its first segments' outputs loaded with their weights.  Few (then each has many
+// segments): a block for two heads, 256 threads: a head's 64 16-byte chunks, four
+// threads for each chunk's segments.  The plan, which was complete before the
+// attend kernel let this one start, is read before the wait for its outputs.
+// Bound by latency: 2 x 1 KB a head and segment.  (A block for each boundary and
+// head, most of them with nothing to do, took 25 us; one for eight heads of a token,
+// four at once, 14.)
 // ===========================================================================
+DEV int plan_entry(const int32_t* p) { return __ldcg(p); }  // (not through L1)
+
+// Segments in pair order of the token b that boundary cb is the first to cut: slot
+// 1 of pair cb - 1 (slot 0 when the token starts its range), slot 0 of every later
+// pair whose range starts inside the token and is not empty.  Called by a warp.
+DEV int segments_of(const Plan& pl, int nc, int cb, int b, uint16_t* slots) {
+  const int lane = threadIdx.x & 31;
+  const int rs = plan_entry(pl.tstart + b), re = plan_entry(pl.tstart + b + 1);
+  int have = 1;
+  if (lane == 0) slots[0] = 2 * (cb - 1) + (rs > plan_entry(pl.tb + cb - 1) ? 1 : 0);
+  for (int c0 = cb; c0 < nc; c0 += 32) {
+    const int c = c0 + lane;
+    const int a = c < nc ? plan_entry(pl.tb + c) : re;
+    const int e = c < nc ? plan_entry(pl.tb + c + 1) : re;
+    const bool in = a < re && e > a;
+    const unsigned m = __ballot_sync(0xffffffffu, in);
+    if (in) slots[have + __popc(m & ((1u << lane) - 1u))] = 2 * c;
+    have += __popc(m);
+    if (!__all_sync(0xffffffffu, a < re)) break;
+  }
+  __syncwarp();
+  return have;
+}
+// the segments' weights of head h into w, by a warp -> their sum
+DEV float segment_weights(const float* lse, const uint16_t* slots, int n, int h, float* w) {
+  const int lane = threadIdx.x & 31;
+  float mx = -INFINITY;
+  for (int i = lane; i < n; i += 32) {
+    const float l = lse[(size_t)slots[i] * kH + h];
+    w[i] = l;
+    mx = fmaxf(mx, l);  // (drops a NaN, which the weights below keep)
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  float sum = 0.f;
+  for (int i = lane; i < n; i += 32) {
+    const float e = w[i] == -INFINITY ? 0.f : exp2f(w[i] - mx);
+    w[i] = e;
+    sum += e;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  __syncwarp();
+  return sum;
+}
+DEV void add_segment(float (&acc)[8], const uint4& v, float w) {
+  const uint32_t p[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    acc[2 * e] += w * u2f(p[e] << 16);
+    acc[2 * e + 1] += w * u2f(p[e] & 0xffff0000u);
+  }
+}
+DEV void store_merged(__nv_bfloat16* dst, const float (&acc)[8], float sum) {
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  *reinterpret_cast<uint4*>(dst) =
+      make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                 pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+}
+
+constexpr int kMergeMany = 16;  // split tokens
+
 __global__ void __launch_bounds__(256) merge_kernel(const __nv_bfloat16* __restrict__ opart,
                                                      const float* __restrict__ lse, const Plan pl,
                                                      int nc, __nv_bfloat16* __restrict__ omerged) {
-  __shared__ int slots[kMaxPairs];
+  __shared__ uint16_t slots[8][kMaxPairs];
+  __shared__ float w[8][kMaxPairs];
   __shared__ int count;
-  __shared__ float w[4][kMaxPairs], wsum[4];
-  __shared__ float acc_s[3][64][8];
-  const int tid = threadIdx.x, ch = tid & 63, g = tid >> 6;
+  __shared__ float wsum, acc_s[3][64][8];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
-  // every block waits, those with nothing to merge too: the value kernel
-  // relies on this grid's completion implying the attend kernel's
-  pdl_wait();
-  const int nsplit = ld_global_nc_s32_early(pl.nact + 1);
-  const bool many = nsplit >= 16;  // four heads at once, each thread all segments
-  const int per = many ? 8 : 2;    // heads of a unit
-  const int units = nsplit * (kH / per);
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int cb = ld_global_nc_s32_early(pl.split + u / (kH / per));
-    const int h0 = u % (kH / per) * per;
-    const int b = ld_global_nc_s32_early(pl.crow + cb);
-    // segments in pair order: slot 1 of pair cb - 1 (slot 0 when the token
-    // starts its range), slot 0 of every later pair whose range starts inside
-    // the token and is not empty
-    if (tid < 32) {
-      const int rs = ld_global_nc_s32_early(pl.tstart + b);
-      const int re = ld_global_nc_s32_early(pl.tstart + b + 1);
-      int have = 1;
-      if (tid == 0)
-        slots[0] = 2 * (cb - 1) + (rs > ld_global_nc_s32_early(pl.tb + cb - 1) ? 1 : 0);
-      for (int c0 = cb; c0 < nc; c0 += 32) {
-        const int c = c0 + tid;
-        const int a = c < nc ? ld_global_nc_s32_early(pl.tb + c) : re;
-        const int e = c < nc ? ld_global_nc_s32_early(pl.tb + c + 1) : re;
-        const bool in = a < re && e > a;
-        const unsigned m = __ballot_sync(0xffffffffu, in);
-        if (in) slots[have + __popc(m & ((1u << tid) - 1u))] = 2 * c;
-        have += __popc(m);
-        if (!__all_sync(0xffffffffu, a < re)) break;
-      }
-      if (tid == 0) count = have;
+  const int nsplit = plan_entry(pl.nact + 1);
+  if (nsplit >= kMergeMany) {
+    int heads = 1;  // of a warp
+    while (heads < kH && (long long)gridDim.x * 8 * heads < (long long)nsplit * kH) heads *= 2;
+    const int unit = (blockIdx.x * 8 + warp) * heads, ti = unit / kH;
+    int b = 0, n = 0;
+    if (ti < nsplit) {
+      const int cb = plan_entry(pl.split + ti);
+      b = plan_entry(pl.crow + cb);
+      n = segments_of(pl, nc, cb, b, slots[warp]);
+    }
+    // every block waits, those with nothing to merge too: the value kernel
+    // relies on this grid's completion implying the attend kernel's
+    pdl_wait();
+    for (int h = unit % kH; n > 0 && h < unit % kH + heads; ++h) {
+      const __nv_bfloat16* src = opart + (size_t)h * kC + lane * 8;
+      uint4 v[3][2];
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            v[i][k] = ld_global_nc_v4(src + (size_t)slots[warp][i] * kH * kC + k * 256);
+      const float sum = segment_weights(lse, slots[warp], n, h, w[warp]);
+      float acc[2][8] = {};
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) add_segment(acc[k], v[i][k], w[warp][i]);
+      for (int i = 3; i < n; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          add_segment(acc[k],
+                      ld_global_nc_v4(src + (size_t)slots[warp][i] * kH * kC + k * 256),
+                      w[warp][i]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        store_merged(omerged + ((size_t)b * kH + h) * kC + k * 256 + lane * 8, acc[k], sum);
+      __syncwarp();
+    }
+    return;
+  }
+  // a token and two heads, in turn
+  const int ch = tid & 63, g = tid >> 6;
+  bool waited = false;
+  for (int u = blockIdx.x; u < nsplit * (kH / 2); u += gridDim.x) {
+    const int cb = plan_entry(pl.split + u / (kH / 2));
+    const int b = plan_entry(pl.crow + cb);
+    if (warp == 0) {
+      const int have = segments_of(pl, nc, cb, b, slots[0]);
+      if (lane == 0) count = have;
     }
     __syncthreads();
     const int n = count;
-    for (int hh = 0; hh < per; hh += many ? 4 : 1) {
-      const int q = many ? g : 0;  // which of the heads at once
-      const int h = h0 + hh + q;
-      // weights: a warp for each head at once
-      if ((tid & 63) < 32 && (many || g == 0)) {
-        const int ln = tid & 31;
-        float mx = -INFINITY;
-        for (int i = ln; i < n; i += 32) {
-          const float l = lse[(size_t)slots[i] * kH + h];
-          w[q][i] = l;
-          mx = fmaxf(mx, l);  // (drops a NaN, which the weights below keep)
-        }
+    if (!waited) pdl_wait();
+    waited = true;
+    for (int h = u % (kH / 2) * 2, last = h + 1; h <= last; ++h) {
+      const __nv_bfloat16* src = opart + (size_t)h * kC + ch * 8;
+      uint4 v[2];  // the thread's first segments: g and g + 4
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        float sum = 0.f;
-        for (int i = ln; i < n; i += 32) {
-          const float e = w[q][i] == -INFINITY ? 0.f : exp2f(w[q][i] - mx);
-          w[q][i] = e;
-          sum += e;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (ln == 0) wsum[q] = sum;
+      for (int k = 0; k < 2; ++k)
+        if (g + 4 * k < n) v[k] = ld_global_nc_v4(src + (size_t)slots[0][g + 4 * k] * kH * kC);
+      if (warp == 0) {
+        const float sum = segment_weights(lse, slots[0], n, h, w[0]);
+        if (lane == 0) wsum = sum;
       }
       __syncthreads();
-      const __nv_bfloat16* src = opart + (size_t)h * kC + ch * 8;
-      float acc[8];
+      float acc[8] = {};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+      for (int k = 0; k < 2; ++k)
+        if (g + 4 * k < n) add_segment(acc, v[k], w[0][g + 4 * k]);
 #pragma unroll 4
-      for (int i = many ? 0 : g; i < n; i += many ? 1 : 4) {
-        const uint4 v = ld_global_nc_v4(src + (size_t)slots[i] * kH * kC);
-        const float wi = w[q][i];
-        const __nv_bfloat162* pv = reinterpret_cast<const __nv_bfloat162*>(&v);
+      for (int i = g + 8; i < n; i += 4)
+        add_segment(acc, ld_global_nc_v4(src + (size_t)slots[0][i] * kH * kC), w[0][i]);
+      if (g > 0)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = __bfloat1622float2(pv[e]);
-          acc[2 * e] += wi * f.x;
-          acc[2 * e + 1] += wi * f.y;
-        }
-      }
-      if (!many) {
-        if (g > 0)
+        for (int e = 0; e < 8; ++e) acc_s[g - 1][ch][e] = acc[e];
+      __syncthreads();
+      if (g == 0) {
+        for (int k = 0; k < 3; ++k)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc_s[g - 1][ch][e] = acc[e];
-        __syncthreads();
-        if (g == 0)
-          for (int k = 0; k < 3; ++k)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] += acc_s[k][ch][e];
-      }
-      if (many || g == 0) {
-        const float inv = wsum[q] == 0.f ? 0.f : 1.f / wsum[q];
-        *reinterpret_cast<uint4*>(omerged + ((size_t)b * kH + h) * kC + ch * 8) =
-            make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv),
-                       pack_bf16x2(acc[2] * inv, acc[3] * inv),
-                       pack_bf16x2(acc[4] * inv, acc[5] * inv),
-                       pack_bf16x2(acc[6] * inv, acc[7] * inv));
+          for (int e = 0; e < 8; ++e) acc[e] += acc_s[k][ch][e];
+        store_merged(omerged + ((size_t)b * kH + h) * kC + ch * 8, acc, wsum);
       }
       __syncthreads();  // w, acc_s and slots may be written again
     }
   }
+  if (!waited) pdl_wait();
 }
 
 // ===========================================================================

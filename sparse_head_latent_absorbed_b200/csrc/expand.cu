@@ -952,16 +952,31 @@ __global__ void __launch_bounds__(256) join_kernel(const Layout ly, const attn::
                                                     int pairs, int head0, int heads,
                                                     __nv_bfloat16* __restrict__ O) {
   using namespace attn;
+  pdl_trigger();
+  // the layout, complete before the attention let this kernel start (not through L1)
+  auto cut_at = [&](int i) {
+    const int2 v = __ldcg(reinterpret_cast<const int2*>(ly.cut + i));
+    return Cut{v.x, v.y};
+  };
+  const int c = blockIdx.x + 1, t = blockIdx.y >> 1, rank = blockIdx.y & 1;
+  const Cut cut = cut_at(c), before = cut_at(c - 1);
+  const bool mine_to_do = cut.j > 0 && !(before.g == cut.g && before.j > 0);
+  const int per = heads / 2;
+  int last = c;  // the pair that holds the item's last piece
+  Block b = {};
+  if (mine_to_do) {
+    for (; last + 1 < pairs; ++last) {
+      const Cut next = cut_at(last + 1);
+      if (next.g != cut.g || next.j == 0) break;
+    }
+    static_assert(sizeof(Block) == 24 && sizeof(Cut) == 8, "read in pairs of words");
+    const int2* src = reinterpret_cast<const int2*>(ly.block + cut.g / per);
+    const int2 x = __ldcg(src), y = __ldcg(src + 1), z = __ldcg(src + 2);
+    b = {x.x, x.y, y.x, y.y, z.x, z.y};
+  }
   // every block waits: the kernel after this one relies on it
   pdl_wait();
-  pdl_trigger();
-  const int c = blockIdx.x + 1, t = blockIdx.y >> 1, rank = blockIdx.y & 1;
-  const Cut cut = ly.cut[c], before = ly.cut[c - 1];
-  if (cut.j == 0 || (before.g == cut.g && before.j > 0)) return;
-  int last = c;  // the pair that holds the item's last piece
-  while (last + 1 < pairs && ly.cut[last + 1].g == cut.g && ly.cut[last + 1].j > 0) ++last;
-  const int per = heads / 2;
-  const Block b = ly.block[cut.g / per];
+  if (!mine_to_do) return;
   const int w = b.width(), tok0 = b.first(t) + rank * w;
   const int mine = min(min(b.n, b.first(t) + 2 * w) - tok0, w);
   const int head = head0 + b.head(t, cut.g % per, heads);
@@ -969,28 +984,48 @@ __global__ void __launch_bounds__(256) join_kernel(const Layout ly, const attn::
     return (size_t)(s < c ? (c - 1) * 2 + 1 : s * 2) * SLOT_ROWS + (t * 2 + rank) * kRows + row;
   };
   const int chunk = threadIdx.x & 15;
-  for (int row = blockIdx.z * 32 + (threadIdx.x >> 4); row < min(mine, (int)blockIdx.z * 32 + 32);
-       row += 16) {
-    float top = -INFINITY;
-    for (int s = c - 1; s <= last; ++s) top = fmaxf(top, parts.lse[at(s, row)]);
+  const int r0 = blockIdx.z * 32 + (threadIdx.x >> 4);  // rows r0 and r0 + 16
+  // the first two pieces (mostly all) with their sums, before anything waits for them
+  float l[2][2];
+  uint4 v[2][2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const size_t x = at(c - 1 + k, r0 + 16 * r);
+      l[r][k] = parts.lse[x];
+      v[r][k] = ld_global_nc_v4(parts.o + x * kD + chunk * 8);
+    }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int row = r0 + 16 * r;
+    if (row >= mine) continue;
+    float top = fmaxf(l[r][0], l[r][1]);
+    for (int s = c + 1; s <= last; ++s) top = fmaxf(top, parts.lse[at(s, row)]);
     float sum = 0.f, acc[8] = {};
-    for (int s = c - 1; s <= last; ++s) {
-      const float lse = parts.lse[at(s, row)];
-      if (lse == -INFINITY) continue;  // (its output is not written)
+    auto add = [&](float lse, const uint4& o) {
+      if (lse == -INFINITY) return;  // (its output is not written)
       const float f = exp2f(lse - top);
-      const uint4 v = *reinterpret_cast<const uint4*>(parts.o + at(s, row) * kD + chunk * 8);
-      const uint32_t p[4] = {v.x, v.y, v.z, v.w};
+      const uint32_t p[4] = {o.x, o.y, o.z, o.w};
       sum += f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         acc[2 * e] += f * u2f(p[e] << 16);
         acc[2 * e + 1] += f * u2f(p[e] & 0xffff0000u);
       }
+    };
+    add(l[r][0], v[r][0]);
+    add(l[r][1], v[r][1]);
+    for (int s = c + 1; s <= last; ++s) {
+      const size_t x = at(s, row);
+      add(parts.lse[x], ld_global_nc_v4(parts.o + x * kD + chunk * 8));
     }
     const float inv = sum > 0.f ? 1.f / sum : sum;  // (0: the token sees nothing; NaN stays)
-    uint4 v = make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
-                         pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
-    *reinterpret_cast<uint4*>(O + ((size_t)(b.tok + tok0 + row) * kH + head) * kD + chunk * 8) = v;
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    *reinterpret_cast<uint4*>(O + ((size_t)(b.tok + tok0 + row) * kH + head) * kD + chunk * 8) =
+        make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 

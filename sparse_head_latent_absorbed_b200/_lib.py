@@ -388,6 +388,13 @@ def _int32(t: torch.Tensor, name: str, dim: int, device) -> torch.Tensor:
     return t
 
 
+def _bf16(t: torch.Tensor, name: str, shape: tuple, device) -> None:
+    if t.dtype != torch.bfloat16 or t.shape != shape or t.device != device or \
+            not t.is_contiguous():
+        raise MLAError(f"{name} must be contiguous bfloat16 {list(shape)} on {device}, got "
+                       f"{t.dtype} {list(t.shape)} on {t.device}")
+
+
 def _status(t: Optional[torch.Tensor], device):
     if t is None:
         return None
@@ -468,16 +475,12 @@ def mla_attend_paged(q_nope: torch.Tensor, q_pe: torch.Tensor, wkv_b: torch.Tens
     int32 [S + 1] (first token of each sequence); kv_len int32 [S] (cached
     positions, the new tokens' own among them), none above max_kv; form "auto",
     "absorbed" or "expanded" -> O bf16 [N,128,128]."""
-    dev = q_nope.device
-    for t, n, shape in ((q_nope, "q_nope", (-1, 128, 128)), (q_pe, "q_pe", (-1, 128, 64)),
-                        (wkv_b, "wkv_b", (128, 256, 512))):
-        _need(t, torch.bfloat16, n)
-        if t.dim() != 3 or t.shape[1:] != shape[1:] or not t.is_contiguous() or t.device != dev:
-            raise MLAError(f"{n} must be contiguous {list(shape)}, on the queries' device")
-    N, S = q_nope.shape[0], kv_len.shape[0] if kv_len.dim() == 1 else -1
-    if q_pe.shape[0] != N or wkv_b.shape[0] != 128:
-        raise MLAError("q_pe must have q_nope's rows, wkv_b 128 heads")
-    _int32(kv_len, "kv_len", 1, dev)
+    _need(q_nope, torch.bfloat16, "q_nope")
+    dev, N = q_nope.device, q_nope.shape[0] if q_nope.dim() else -1
+    _bf16(q_nope, "q_nope", (N, 128, 128), dev)
+    _bf16(q_pe, "q_pe", (N, 128, 64), dev)
+    _bf16(wkv_b, "wkv_b", (128, 256, 512), dev)
+    S = _int32(kv_len, "kv_len", 1, dev).shape[0]
     if _int32(cu_q, "cu_q", 1, dev).shape[0] != S + 1:
         raise MLAError("cu_q must have one entry more than kv_len")
     if _int32(page_table, "page_table", 2, dev).shape[0] != S or pages.device != dev:
@@ -486,18 +489,20 @@ def mla_attend_paged(q_nope: torch.Tensor, q_pe: torch.Tensor, wkv_b: torch.Tens
         raise MLAError(f"form must be one of {', '.join(FORMS)}")
     if out is None:
         out = torch.empty_like(q_nope)
-    _need(out, torch.bfloat16, "out")
-    if out.shape != q_nope.shape or not out.is_contiguous() or out.device != dev:
-        raise MLAError("out must be contiguous [N, 128, 128], on the queries' device")
+    else:
+        _bf16(out, "out", (N, 128, 128), dev)
     if N == 0 or S == 0:
         return out
     if ws is not None and (ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != dev):
         raise MLAError("ws must be contiguous uint8, on the queries' device")
     pool, kind, P, ps, page, row = _pool(pages)
     if ws is None:
-        # (some sizes depend on the device's SM count)
-        with torch.cuda.device(dev):
-            need = mla_attend_paged_workspace_bytes(N, S, max_kv, 8 if kind else 16, form)
+        sizes = (N, S, max_kv, 8 if kind else 16, form)
+        if torch.cuda.current_device() == dev.index:
+            need = mla_attend_paged_workspace_bytes(*sizes)
+        else:  # (some sizes depend on the device's SM count)
+            with torch.cuda.device(dev):
+                need = mla_attend_paged_workspace_bytes(*sizes)
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
     _on_device(dev, "mla_attend_paged", LIB.mla_attend_paged, q_nope.data_ptr(), q_pe.data_ptr(),
                wkv_b.data_ptr(), pool, kind, P, ps, page, row, page_table.data_ptr(),

@@ -367,6 +367,29 @@ def test_captured_call_that_converts_its_pages(shla):
         assert (out[34:] == 7).all()
 
 
+def test_captured_expanded_call_with_split_work(shla):
+    # long enough that several pairs share an item and their outputs are joined
+    w = R.make([300, 40, 0], [2500, 1300, 70], 16, 64, 28, pad_tokens=2)
+    N, full, w["max_kv"] = w["q_nope"].shape[0], w["kv_len"].clone(), 4000
+    ws = torch.empty(shla.mla_attend_paged_workspace_bytes(N, 3, 4000, 16, "expanded"),
+                     dtype=torch.uint8, device="cuda")
+    out = torch.full_like(w["q_nope"], 7.0)
+    shla.mla_attend_paged(**w, form="expanded", out=out, ws=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        shla.mla_attend_paged(**w, form="expanded", out=out, ws=ws)
+    for cut in (1200, 0, 77):
+        w["kv_len"].copy_((full - cut).clamp(min=0))
+        out.fill_(7.0)
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(out[:340], ref_of(w)[:340])
+        assert (out[340:] == 7).all()
+        assert torch.equal(shla.mla_attend_paged(**w, form="expanded")[:340], out[:340])
+
+
 @pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("bits", [16, 8])
 def test_sequences_that_share_pages(shla, form, bits):

@@ -962,26 +962,38 @@ __global__ void __launch_bounds__(256) join_kernel(const Layout ly, const attn::
   const Cut cut = cut_at(c), before = cut_at(c - 1);
   const bool mine_to_do = cut.j > 0 && !(before.g == cut.g && before.j > 0);
   const int per = heads / 2;
-  int last = c;  // the pair that holds the item's last piece
+  // The pairs that hold a piece of the item, in its order.  Not all from the first
+  // to the last do: with less work than pairs neighbouring cuts coincide, and the
+  // pair between them has nothing and writes nothing.
+  __shared__ int piece[kPairs], pieces;
   Block b = {};
   if (mine_to_do) {
-    for (; last + 1 < pairs; ++last) {
-      const Cut next = cut_at(last + 1);
-      if (next.g != cut.g || next.j == 0) break;
+    if (threadIdx.x == 0) {
+      int n = 0;
+      piece[n++] = c - 1;
+      Cut at = cut;
+      for (int s = c; s < pairs && at.g == cut.g && at.j > 0; ++s) {
+        const Cut next = cut_at(s + 1);
+        if (next.g != at.g || next.j != at.j) piece[n++] = s;
+        at = next;
+      }
+      pieces = n;
     }
     static_assert(sizeof(Block) == 24 && sizeof(Cut) == 8, "read in pairs of words");
     const int2* src = reinterpret_cast<const int2*>(ly.block + cut.g / per);
     const int2 x = __ldcg(src), y = __ldcg(src + 1), z = __ldcg(src + 2);
     b = {x.x, x.y, y.x, y.y, z.x, z.y};
   }
+  __syncthreads();
   // every block waits: the kernel after this one relies on it
   pdl_wait();
   if (!mine_to_do) return;
+  const int n = pieces;  // two or more
   const int w = b.width(), tok0 = b.first(t) + rank * w;
   const int mine = min(min(b.n, b.first(t) + 2 * w) - tok0, w);
   const int head = head0 + b.head(t, cut.g % per, heads);
-  auto at = [&](int s, int row) {  // piece s: the first is its pair's last, the others their pairs' first
-    return (size_t)(s < c ? (c - 1) * 2 + 1 : s * 2) * SLOT_ROWS + (t * 2 + rank) * kRows + row;
+  auto at = [&](int k, int row) {  // piece k: the first is its pair's last, the others their pairs' first
+    return (size_t)(piece[k] * 2 + (k == 0 ? 1 : 0)) * SLOT_ROWS + (t * 2 + rank) * kRows + row;
   };
   const int chunk = threadIdx.x & 15;
   const int r0 = blockIdx.z * 32 + (threadIdx.x >> 4);  // rows r0 and r0 + 16
@@ -992,7 +1004,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Layout ly, const attn::
   for (int r = 0; r < 2; ++r)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const size_t x = at(c - 1 + k, r0 + 16 * r);
+      const size_t x = at(k, r0 + 16 * r);
       l[r][k] = parts.lse[x];
       v[r][k] = ld_global_nc_v4(parts.o + x * kD + chunk * 8);
     }
@@ -1001,7 +1013,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Layout ly, const attn::
     const int row = r0 + 16 * r;
     if (row >= mine) continue;
     float top = fmaxf(l[r][0], l[r][1]);
-    for (int s = c + 1; s <= last; ++s) top = fmaxf(top, parts.lse[at(s, row)]);
+    for (int k = 2; k < n; ++k) top = fmaxf(top, parts.lse[at(k, row)]);
     float sum = 0.f, acc[8] = {};
     auto add = [&](float lse, const uint4& o) {
       if (lse == -INFINITY) return;  // (its output is not written)
@@ -1016,8 +1028,8 @@ __global__ void __launch_bounds__(256) join_kernel(const Layout ly, const attn::
     };
     add(l[r][0], v[r][0]);
     add(l[r][1], v[r][1]);
-    for (int s = c + 1; s <= last; ++s) {
-      const size_t x = at(s, row);
+    for (int k = 2; k < n; ++k) {
+      const size_t x = at(k, row);
       add(parts.lse[x], ld_global_nc_v4(parts.o + x * kD + chunk * 8));
     }
     const float inv = sum > 0.f ? 1.f / sum : sum;  // (0: the token sees nothing; NaN stays)

@@ -53,7 +53,8 @@ enum {
   MLA_ERR_ALIGN = -3,       /* a pointer or stride breaks 16-byte alignment */
   MLA_ERR_WORKSPACE = -4,   /* workspace pointer NULL or too small */
   MLA_ERR_UNSUPPORTED = -5, /* device is not sm_100 */
-  MLA_ERR_CUDA = -6         /* a CUDA launch or attribute call failed */
+  MLA_ERR_CUDA = -6,        /* a CUDA launch or attribute call failed */
+  MLA_ERR_OVERLAP = -7      /* an output or the workspace shares memory with another argument */
 };
 
 #define MLA_STATUS_TIMEOUT 1
@@ -396,7 +397,9 @@ int mla_query_proj(const mla_bf16_t* x, const mla_bf16_t* wq_a, const mla_bf16_t
  *   rows   bf16, row i at rows + i*rstride (rstride in elements, a multiple of 8, >= 576)
  *   slots  int32 [N]; -1 skips the row, any other slot outside the pool is
  *          skipped and counted in status[1].  Slots are distinct: of a slot
- *          listed twice, each 16-byte piece holds one of the two rows'.
+ *          listed twice, each 16-byte piece holds one of the two rows'.  Rows
+ *          may themselves lie in the pool (a page copied to another), but not
+ *          in a slot that the call writes.
  * The scale of a group is the least power of two 2^n, -117 <= n <= 119, with
  * max |x| <= 448 * 2^n over the group; a code is x / scale (exact) rounded to
  * nearest even, saturated at 448.  A group with an infinity or NaN gets the
@@ -407,7 +410,8 @@ int mla_query_proj(const mla_bf16_t* x, const mla_bf16_t* wq_a, const mla_bf16_t
  *
  * mla_page_read returns the rows of slots as bf16 [N] rows (exactly code *
  * scale); slot -1, and any other slot outside the pool (counted in
- * status[1]), gives a row of zeros.
+ * status[1]), gives a row of zeros.  The rows written
+ * share no memory with the slots read.
  *
  * Both enqueue one kernel and use no workspace.
  */
@@ -451,6 +455,9 @@ int mla_page_read(const void* pool, int kind, int num_pages, int page_size, int6
  *              The forms agree within rounding.
  *   ws         at least mla_attend_paged_workspace_bytes(N, S, max_kv, kind,
  *              form) bytes, 256-byte aligned; contents need not be initialised
+ *   O and ws   share no memory with each other and with the arguments that are
+ *              read (else MLA_ERR_OVERLAP; the pool's rows, which may lie among
+ *              other memory, are not looked at)
  *   status     optional int32[2].  An entry of page_table outside [0, num_pages)
  *              for a page below a sequence's length reads as a page of zeros
  *              and is counted once in status[1].

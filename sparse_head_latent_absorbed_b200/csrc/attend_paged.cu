@@ -1409,9 +1409,25 @@ extern "C" int mla_attend_paged(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe
   if (!aligned16(q_nope) || !aligned16(q_pe) || !aligned16(wkv_b) || !aligned16(O))
     return MLA_ERR_ALIGN;
   if (!ws || !aligned256(ws)) return MLA_ERR_WORKSPACE;
+  const size_t need = mla_attend_paged_workspace_bytes(N, S, max_kv, kind, form);
+  // (the expanded form stores outputs while other SMs still load queries, and reads
+  // all others after its first ones too)
+  const size_t row = (size_t)MLA_HEADS * 2 * MLA_NOPE, out_bytes = N * row;
+  const struct {
+    const void* p;
+    size_t bytes;
+  } inputs[] = {{q_nope, N * row},
+                {q_pe, (size_t)N * MLA_HEADS * 2 * MLA_ROPE},
+                {wkv_b, (size_t)MLA_HEADS * 256 * MLA_LATENT * 2},
+                {page_table, (size_t)S * max_pages * 4},
+                {cu_q, ((size_t)S + 1) * 4},
+                {kv_len, (size_t)S * 4}};
+  for (const auto& in : inputs)
+    if (overlap(O, out_bytes, in.p, in.bytes) || overlap(ws, need, in.p, in.bytes))
+      return MLA_ERR_OVERLAP;
+  if (overlap(O, out_bytes, ws, need)) return MLA_ERR_OVERLAP;
   if (int e = check_device()) return e;
-  if (ws_bytes < mla_attend_paged_workspace_bytes(N, S, max_kv, kind, form))
-    return MLA_ERR_WORKSPACE;
+  if (ws_bytes < need) return MLA_ERR_WORKSPACE;
   paged::Pool p;
   p.base = static_cast<const uint8_t*>(pool);
   p.kind = kind;

@@ -104,6 +104,7 @@ extern "C" const char* mla_status_string(int code) {
     case MLA_ERR_WORKSPACE: return "workspace is NULL, misaligned or too small";
     case MLA_ERR_UNSUPPORTED: return "device is not compute capability 10.0 (sm_100a)";
     case MLA_ERR_CUDA: return "a CUDA call or kernel launch failed";
+    case MLA_ERR_OVERLAP: return "an output or the workspace shares memory with another argument";
     default: return "unknown status code";
   }
 }

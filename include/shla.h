@@ -450,9 +450,11 @@ int mla_page_read(const void* pool, int kind, int num_pages, int page_size, int6
  *              MLA_FORM_EXPANDED computes every position's keys and values of
  *              the 128 heads once (33.6 Mflop a position) and attends to those
  *              (81,920 flop per token and position).  MLA_FORM_AUTO takes the
- *              expanded form, where it is not refused, from an average of 112
- *              (max_kv <= 1024), 160 (<= 4096) or 208 new tokens a sequence on.
- *              The forms agree within rounding.
+ *              expanded form from an average of 112 (max_kv <= 1024), 160
+ *              (<= 4096) or 208 new tokens a sequence on, where S * max_kv, each
+ *              length rounded up to 128, is at most 2^21 (its workspace then
+ *              takes up to 11 GB) or the absorbed form is refused.  The forms
+ *              agree within rounding.
  *   ws         at least mla_attend_paged_workspace_bytes(N, S, max_kv, kind,
  *              form) bytes, 256-byte aligned; contents need not be initialised
  *   O and ws   share no memory with each other and with the arguments that are

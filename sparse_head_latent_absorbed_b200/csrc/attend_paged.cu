@@ -1365,10 +1365,18 @@ static int run_absorbed(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const 
 
 using namespace shla;
 
-// The form of a call: as asked, or by the new tokens per sequence.
+// The absorbed form's list of (token, 128-key tile) is counted in 32 bits.
+static bool absorbed_fits(int N, int max_kv) {
+  return (int64_t)N * ((max_kv + 127) / 128) <= 0x3fffffff;
+}
+
+// The form of a call: as asked, or by the new tokens per sequence.  Past
+// kAutoRows positions in all the expanded form's workspace decides, not its time.
 static int form_of(int form, int N, int S, int max_kv) {
   if (form != MLA_FORM_AUTO) return form;
-  return (int64_t)N >= (int64_t)S * expand::min_tokens(max_kv) && expand::fits(S, max_kv)
+  if ((int64_t)N < (int64_t)S * expand::min_tokens(max_kv)) return MLA_FORM_ABSORBED;
+  return expand::fits(S, max_kv, expand::kAutoRows) ||
+                 (!absorbed_fits(N, max_kv) && expand::fits(S, max_kv))
              ? MLA_FORM_EXPANDED
              : MLA_FORM_ABSORBED;
 }
@@ -1378,10 +1386,8 @@ static int check_sizes(int N, int S, int max_kv, int kind, int form) {
   if (N < 1 || N > 65535 || S < 1 || S > 65535 || max_kv < 1 || max_kv > (1 << 24))
     return MLA_ERR_SHAPE;
   if (form < MLA_FORM_AUTO || form > MLA_FORM_EXPANDED) return MLA_ERR_SHAPE;
-  // absorbed: the flattened list of (token, 128-key tile) is counted in 32 bits
-  if (form_of(form, N, S, max_kv) == MLA_FORM_EXPANDED
-          ? !expand::fits(S, max_kv)
-          : (int64_t)N * ((max_kv + 127) / 128) > 0x3fffffff)
+  if (form_of(form, N, S, max_kv) == MLA_FORM_EXPANDED ? !expand::fits(S, max_kv)
+                                                       : !absorbed_fits(N, max_kv))
     return MLA_ERR_SHAPE;
   return MLA_OK;
 }

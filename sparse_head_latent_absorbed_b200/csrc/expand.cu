@@ -1085,8 +1085,8 @@ static Ws layout(int N, int S, int max_kv) {
   return w;
 }
 
-bool fits(int S, int max_kv) {
-  return (int64_t)S * ((max_kv + kRows - 1) / kRows * kRows) <= kMaxRows;
+bool fits(int S, int max_kv, int64_t rows) {
+  return (int64_t)S * ((max_kv + kRows - 1) / kRows * kRows) <= rows;
 }
 
 size_t workspace_bytes(int N, int S, int max_kv) { return layout(N, S, max_kv).total; }

@@ -16,7 +16,12 @@ inline int min_tokens(int max_kv) { return max_kv <= 1024 ? 112 : max_kv <= 4096
 
 // Positions of all sequences, each rounded up to 128, that a call may reach.
 constexpr int64_t kMaxRows = 1 << 26;
-bool fits(int S, int max_kv);
+// ... and may reach for MLA_FORM_AUTO to expand: a workspace of 11 GB, 6% of the
+// GPU's memory (16 sequences of 131,072 positions, 512 new tokens each: 140 ms
+// against 318 absorbed).  It grows by 5.2 KB a position: 176 GB for 256 sequences
+// under that bound, however short they are, which the absorbed form serves from 17.
+constexpr int64_t kAutoRows = 1 << 21;
+bool fits(int S, int max_kv, int64_t rows = kMaxRows);
 
 size_t workspace_bytes(int N, int S, int max_kv);
 

@@ -16,6 +16,7 @@
 
 #include "attend_paged.cuh"
 #include "expand.h"
+#include "fold.h"
 #include "pair.cuh"
 #include "tma_map.h"
 
@@ -1330,7 +1331,8 @@ static int run_absorbed(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const 
   __nv_bfloat16* q_tilde = reinterpret_cast<__nv_bfloat16*>(ws + L.q_tilde);
   // The fold waits for the stream's earlier work as usual; the others may start
   // while their predecessor drains.
-  if (int e = mla_fold_wuk(q_nope, wkv_b, q.N, reinterpret_cast<mla_bf16_t*>(q_tilde), st))
+  if (int e = launch_fold(reinterpret_cast<const __nv_bfloat16*>(q_nope),
+                          reinterpret_cast<const __nv_bfloat16*>(wkv_b), q_tilde, q.N, status, st))
     return e;
   if (int e = launch_pdl(plan_kernel, dim3(1), dim3(1024), 0, st, q, pool, pl, nc)) return e;
   Params p;

@@ -19,6 +19,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "fold.h"
 #include "host_util.h"
 
 namespace shla {
@@ -1374,8 +1375,8 @@ static int launch_fold_nb(const __nv_bfloat16* q_nope, const __nv_bfloat16* wkv_
   return launch_status();
 }
 
-static int launch_fold(const __nv_bfloat16* q_nope, const __nv_bfloat16* wkv_b,
-                       __nv_bfloat16* q_tilde, int B, int32_t* status, cudaStream_t st) {
+int launch_fold(const __nv_bfloat16* q_nope, const __nv_bfloat16* wkv_b, __nv_bfloat16* q_tilde,
+                int B, int32_t* status, cudaStream_t st) {
   if (B <= 16) return launch_fold_nb<16>(q_nope, wkv_b, q_tilde, B, status, st);
   if (B <= 32) return launch_fold_nb<32>(q_nope, wkv_b, q_tilde, B, status, st);
   if (B <= 64) return launch_fold_nb<64>(q_nope, wkv_b, q_tilde, B, status, st);

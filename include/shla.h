@@ -472,12 +472,14 @@ int mla_page_read(const void* pool, int kind, int num_pages, int page_size, int6
  * 128, at most 2^26 (else MLA_ERR_SHAPE).  The expanded form's workspace holds
  * 1152 bytes for each of those positions and the keys and values of as many
  * heads as fit 4 GiB, at least 8 (4 KB a position) and at most 128 (64 KB),
- * and 20 MB of partial outputs.
+ * and 20 MB of partial outputs (40 MB for max_kv above 2^17).
  * The absorbed form on 8-bit pages with three tokens a sequence or more on
  * average (N >= 3 S, N * max_kv >= 2^18) converts the positions to bf16 in the
  * workspace first, 1152 bytes each, where that is 4 GiB at most.
  *
- * Arithmetic: scores, softmax statistics and outputs accumulate in fp32.
+ * Arithmetic: scores, softmax statistics and outputs accumulate in fp32; the
+ * tensor cores' additions truncate, so an output's sum is moved to another one,
+ * added to nearest, every 2^17 positions.
  * Rounded to bf16, as tensor-core operands: softmax weights; absorbed: q~, the
  * mixed latent and a split token's partial mixed latents; expanded: keys,
  * values and the partial outputs of work that is split between SMs.  On one device a call gives the same bits every time.

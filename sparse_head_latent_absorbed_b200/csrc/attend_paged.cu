@@ -200,6 +200,7 @@ constexpr int OFF_P = OFF_V + 2 * V_CHUNK;
 constexpr int SMEM_BYTES = OFF_P + 2 * P_BYTES;
 constexpr uint32_t T_S = 0, T_O = 256, TMEM_COLS = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr int ACC = 128 * 256 + 128;  // [256 / 4 columns][128 lanes][4], then the lanes' maxima
 static_assert(OFF_K % 1024 == 0 && OFF_V % 1024 == 0 && OFF_P % 1024 == 0, "alignment");
 static_assert(T_S + NSB * KT / 2 <= T_O, "TMEM plan");
 constexpr int KEY_WARP0 = 8;
@@ -225,6 +226,7 @@ struct Params {
   __nv_bfloat16* opart;          // [pairs][2 slots][128][512], normalised per segment
   float* lse;                    // [pairs][2 slots][128], log2 units of scaled scores
   __nv_bfloat16* omerged;        // [N][128][512]
+  float* acc;                    // [pairs][2 CTAs] x ACC: accumulators taken out of TMEM
   int32_t* status;
 };
 
@@ -650,7 +652,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::thread
       bool ok = true;
 #pragma unroll 1
       for (int i = 0; i < n && ok; ++i) {
-        const uint32_t first = i == 0 || jt == 0 ? 1u : 0u;
+        const uint32_t first = (jt - (bb == bb0 ? jt0 : 0)) % kRun == 0 ? 1u : 0u;
 #pragma unroll 1
         for (int c = 0; c < 2 && ok; ++c) {  // half of the keys
           ok = warp_wait(&bars.v_full[c], i & 1, abort, p.status) &&
@@ -718,6 +720,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::thread
     int bb = bb0, jt = jt0, nr = tiles_of(bb0), lim = lim_of(bb0);
     int nseg = 0;  // tokens whose last tile came before this one
     int lseg = 0;  // the segment that l belongs to
+    // this lane's part of the accumulator's copy and the maximum it refers to.  A
+    // segment's runs end at every kRun-th tile, always of the same group: each thread
+    // reads what it wrote, and what the other group's wrote only at the segment's end.
+    static_assert(kRun % 2 == 0, "runs end at tiles of one group");
+    float* const acc = p.acc + (size_t)blockIdx.x * ACC;
+    float4* const acc4 = reinterpret_cast<float4*>(acc) + ln;
+    float* const acc_m = acc + 128 * 256 + ln;
     auto step = [&]() {
       if (++jt == nr) {
         jt = 0;
@@ -730,7 +739,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::thread
 #pragma unroll 1
     for (int i = g; i < n; i += 2) {
       const int ph = (i >> 1) & 1;
-      const bool first = i == 0 || jt == 0;          // the segment's first tile
+      const int js = jt - (nseg == 0 ? jt0 : 0);     // tile of the segment
+      const bool first = js == 0;
       const bool ends = jt == nr - 1 || i == n - 1;  // ... its last
       if (nseg != lseg) {  // this group's first tile of the segment
         lseg = nseg;
@@ -775,7 +785,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::thread
       const bool raise = mt > m + kRescaleThreshold;
       const float mn = raise ? mt : m;
       if (!ends) publish_m(mn);
-      if (!first && __any_sync(0xffffffffu, raise)) {
+      if (!first && js % kRun == 0) {
+        // a run ends: O~, which holds all tiles up to i - 1, moves to its copy
+        if (!wait_pv(i - 1)) break;
+        const bool more = js > kRun;
+        float a = 0.f;
+        if (more) {
+          const float am = __ldcg(acc_m);
+          a = am == m ? 1.f : fast_exp2(am - m);
+        }
+#pragma unroll 1
+        for (int cc = 0; cc < 256; cc += 16) {
+          uint32_t r[16];
+          tmem_ld16(to + cc, r);
+          tc_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float4 v = more ? __ldcg(acc4 + (cc / 4 + k) * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v.x = v.x * a + u2f(r[4 * k]);
+            v.y = v.y * a + u2f(r[4 * k + 1]);
+            v.z = v.z * a + u2f(r[4 * k + 2]);
+            v.w = v.w * a + u2f(r[4 * k + 3]);
+            __stcg(acc4 + (cc / 4 + k) * 128, v);
+          }
+        }
+        __stcg(acc_m, m);
+      } else if (!first && __any_sync(0xffffffffu, raise)) {
         // O~ must hold the value product of tile i - 1 before it is scaled
         if (!wait_pv(i - 1)) break;
         const float a = raise ? fast_exp2(m - mn) : 1.f;
@@ -876,6 +911,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::thread
         const int slot = 2 * cid + (nseg == 0 ? 0 : 1);
         const int head = rank * HH + h;
         const float inv = lt == 0.f ? 0.f : 1.f / lt;
+        const bool moved = js >= kRun;  // earlier runs' part is in the copy
+        float a = 0.f;
+        if (moved) {
+          const float am = __ldcg(acc_m);
+          a = am == mn ? 1.f : fast_exp2(am - mn);
+        }
         __nv_bfloat16* dst = (!partial ? p.omerged + ((size_t)bb * kH + head) * kC
                                        : p.opart + ((size_t)slot * kH + head) * kC) +
                              half * 256;
@@ -884,6 +925,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::thread
           uint32_t r[32];
           tmem_ld32(to + cc, r);
           tc_wait_ld();
+          if (moved) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float4 v = __ldcg(acc4 + (cc / 4 + k) * 128);
+              r[4 * k] = f2u(u2f(r[4 * k]) + v.x * a);
+              r[4 * k + 1] = f2u(u2f(r[4 * k + 1]) + v.y * a);
+              r[4 * k + 2] = f2u(u2f(r[4 * k + 2]) + v.z * a);
+              r[4 * k + 3] = f2u(u2f(r[4 * k + 3]) + v.w * a);
+            }
+          }
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             *reinterpret_cast<uint4*>(dst + cc + 8 * j) = make_uint4(
@@ -1236,7 +1287,7 @@ static int max_pairs() {
 }
 
 struct AbsorbedWs {
-  size_t q_tilde, opart, lse, omerged, seq, lim, tstart, tb, crow, split, nact, total;
+  size_t q_tilde, opart, lse, acc, omerged, seq, lim, tstart, tb, crow, split, nact, total;
 };
 
 static AbsorbedWs absorbed_ws(int N, int nc) {
@@ -1244,7 +1295,8 @@ static AbsorbedWs absorbed_ws(int N, int nc) {
   w.q_tilde = 0;
   w.opart = round_up((size_t)N * kH * kC * 2, 256);
   w.lse = w.opart + (size_t)nc * 2 * kH * kC * 2;
-  w.omerged = round_up(w.lse + (size_t)nc * 2 * kH * 4, 256);
+  w.acc = round_up(w.lse + (size_t)nc * 2 * kH * 4, 256);
+  w.omerged = round_up(w.acc + (size_t)nc * 2 * ACC * 4, 256);
   w.seq = round_up(w.omerged + (size_t)N * kH * kC * 2, 256);
   w.lim = round_up(w.seq + (size_t)N * 4, 256);
   w.tstart = round_up(w.lim + (size_t)N * 4, 256);
@@ -1346,6 +1398,7 @@ static int run_absorbed(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const 
   p.scale_log2 = scale * 1.4426950408889634f;
   p.opart = reinterpret_cast<__nv_bfloat16*>(ws + L.opart);
   p.lse = reinterpret_cast<float*>(ws + L.lse);
+  p.acc = reinterpret_cast<float*>(ws + L.acc);
   p.omerged = reinterpret_cast<__nv_bfloat16*>(ws + L.omerged);
   p.status = status;
   if (int e = pool.kind == MLA_PAGE_E4M3 ? launch_absorbed<true>(p, nc, st)

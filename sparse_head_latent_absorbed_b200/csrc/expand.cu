@@ -29,6 +29,7 @@ using paged::kC;
 using paged::kD;
 using paged::kH;
 using paged::kR;
+using paged::kRun;
 using paged::Pool;
 using paged::Seqs;
 
@@ -552,7 +553,9 @@ constexpr int SLOT_ROWS = 4 * kRows;
 struct Parts {
   __nv_bfloat16* o;  // [pairs][2][2][2][128][128]
   float* lse;        // [pairs][2][2][2][128]
+  float* acc;        // [pairs][2 CTAs][2 tiles] x ACC: accumulators taken out of TMEM
 };
+constexpr int ACC = 128 * 128 + 2 * 128;  // [128 / 4 columns][128 rows][4], then maximum and sum of the rows
 }  // namespace attn
 
 // D (+)= A B with A in TMEM: each CTA of the pair its own rows at the same address
@@ -564,6 +567,46 @@ DEV void tc_mma2_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
       "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "n"(kAccumulate ? 1 : 0)
       : "memory");
+}
+
+// This softmax thread's place in the copies of the accumulators: its row's
+// columns, in pieces of four 128 apart, and its maximum and sum.
+DEV float4* acc_of(float* acc) {
+  return reinterpret_cast<float4*>(acc + (size_t)(blockIdx.x * 2 + (threadIdx.x >> 7)) * attn::ACC) +
+         (threadIdx.x & 127);
+}
+DEV float2* acc_sum_of(float* acc) {
+  return reinterpret_cast<float2*>(
+             acc + (size_t)(blockIdx.x * 2 + (threadIdx.x >> 7)) * attn::ACC + 128 * 128) +
+         (threadIdx.x & 127);
+}
+// Adds the row's output in TMEM and its sum, both relative to the maximum m, to
+// the copies (which hold earlier runs if `more`).  Out of line: inlined it costs
+// the loop over the tiles registers.
+static __device__ __noinline__ void end_run(uint32_t to, float* acc, float m, float l, bool more) {
+  float4* const dst = acc_of(acc);
+  float a = 0.f;
+  if (more) {
+    const float2 ml = __ldcg(acc_sum_of(acc));
+    a = ml.x == m ? 1.f : fast_exp2(ml.x - m);
+    l += ml.y * a;
+  }
+#pragma unroll 1
+  for (int c = 0; c < 128; c += 16) {
+    uint32_t o[16];
+    tmem_ld16(to + c, o);
+    tc_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float4 v = more ? __ldcg(dst + (c / 4 + k) * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v.x = v.x * a + u2f(o[4 * k]);
+      v.y = v.y * a + u2f(o[4 * k + 1]);
+      v.z = v.z * a + u2f(o[4 * k + 2]);
+      v.w = v.w * a + u2f(o[4 * k + 3]);
+      __stcg(dst + (c / 4 + k) * 128, v);
+    }
+  }
+  __stcg(acc_sum_of(acc), make_float2(m, l));
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
@@ -757,7 +800,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
         for (int j = 0; j < nt[1] && ok; ++j)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (j < nt[t] && ok) value(t, at(t, j), j == 0, two || t == 1, j + 1 == nt[t]);
+            if (j < nt[t] && ok)
+              value(t, at(t, j), j % kRun == 0, two || t == 1, j + 1 == nt[t]);
             if (j + 1 < nt[t] && ok) score(t, at(t, j + 1), two || t == 1, j + 2 == nt[t]);
           }
         u0 += nt[1] * per_j;
@@ -821,6 +865,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
           mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) *
                scale_log2;
         }
+        if (j > w.j0 && (j - w.j0) % kRun == 0) {
+          // a run ends: the output so far and its sum, relative to the maximum before
+          // this tile, move to their copies
+          float x, y;
+          unpack2(add2(la, lb), x, y);
+          end_run(to, parts.acc, m, x + y, j - w.j0 > kRun);
+          la = lb = 0;
+        }
         const bool raise = mt > m + kRescaleThreshold;
         if (__any_sync(0xffffffffu, raise)) {
           // (the value products before these scores have completed with them)
@@ -876,11 +928,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
         }
       }
       if (!ok) break;
-      float inv = 0.f;
+      const bool moved = nt > kRun;  // earlier runs' part is in the copy
+      float inv = 0.f, l = 0.f, a = 0.f;
       if (nt > 0) {
         float x, y;
         unpack2(add2(la, lb), x, y);
-        const float l = x + y;
+        l = x + y;
+        if (moved) {
+          const float2 ml = __ldcg(acc_sum_of(parts.acc));
+          a = ml.x == m ? 1.f : fast_exp2(ml.x - m);
+          l += ml.y * a;
+        }
         inv = l == 0.f ? 0.f : 1.f / l;
         ok = warp_wait(&bars.o_full[t], on & 1, abort, status);
         ++on;
@@ -894,9 +952,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
       } else {
         const size_t at = (size_t)(pair * 2 + (w.j0 > 0 ? 0 : 1)) * SLOT_ROWS +
                           (t * 2 + rank) * kRows + row;
-        float x, y;
-        unpack2(add2(la, lb), x, y);
-        const float l = nt > 0 ? x + y : 0.f;
         parts.lse[at] = l == 0.f ? -INFINITY : m + log2f(l);
         dst = parts.o + at * kD;
         store = store && nt > 0;
@@ -907,6 +962,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
         if (nt > 0) {
           tmem_ld32(to + c, o);
           tc_wait_ld();
+        }
+        if (moved) {
+          const float4* const src = acc_of(parts.acc);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float4 v = __ldcg(src + (c / 4 + k) * 128);
+            o[4 * k] = f2u(u2f(o[4 * k]) + v.x * a);
+            o[4 * k + 1] = f2u(u2f(o[4 * k + 1]) + v.y * a);
+            o[4 * k + 2] = f2u(u2f(o[4 * k + 2]) + v.z * a);
+            o[4 * k + 3] = f2u(u2f(o[4 * k + 3]) + v.w * a);
+          }
         }
         if (store) {
 #pragma unroll
@@ -1068,7 +1134,7 @@ static RowsWs rows_ws(int N, int S, int max_kv) {
 
 struct Ws {
   RowsWs r;
-  size_t k, v, parts, lse, total;
+  size_t k, v, parts, lse, acc, total;
   int heads;  // of a group
 };
 
@@ -1081,7 +1147,8 @@ static Ws layout(int N, int S, int max_kv) {
   w.v = w.k + (size_t)w.r.max_rows * w.heads * kD * 2;
   w.parts = w.v + (size_t)w.r.max_rows * w.heads * kD * 2;
   w.lse = w.parts + (size_t)kPairs * 2 * attn::SLOT_ROWS * kD * 2;
-  w.total = w.lse + (size_t)kPairs * 2 * attn::SLOT_ROWS * 4;
+  w.acc = w.lse + (size_t)kPairs * 2 * attn::SLOT_ROWS * 4;
+  w.total = w.acc + (max_kv > kRun * kRows ? (size_t)kPairs * 4 * attn::ACC * 4 : 0);
   return w;
 }
 
@@ -1176,7 +1243,8 @@ int run(const mla_bf16_t* q_nope, const mla_bf16_t* q_pe, const mla_bf16_t* wkv_
   const dim3 grid(2 * (sms / 2));
   const int pairs = pairs_of(sms);
   const attn::Parts parts = {reinterpret_cast<__nv_bfloat16*>(ws + L.parts),
-                             reinterpret_cast<float*>(ws + L.lse)};
+                             reinterpret_cast<float*>(ws + L.lse),
+                             reinterpret_cast<float*>(ws + L.acc)};
   __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(O);
   for (int h0 = 0; h0 < kH; h0 += L.heads) {
     if (int e = launch_pdl(expand_kernel, grid, dim3(gemm::THREADS), gemm::SMEM, st, map_c, map_w,

@@ -579,9 +579,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::thread
     // ---------------- queries: this CTA's 64 heads of each token ----------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::rest));
     const uint32_t bar = first_cta(&bars.q_full);
-    int bb = bb0, i = 0;
+    int bb = bb0, i = 0, use = 0;  // use: tiles of the segment before
     for (int seg = 0; i < n; ++seg, ++bb) {
-      if (!warp_wait(&bars.q_free, (seg & 1) ^ 1, abort, p.status)) break;
+      if (!warp_wait(&bars.q_free, (seg & 1) ^ 1, abort, p.status, queries_limit_ns(use))) break;
       if (lane == 0) {
         if (rank == 0) mbar_arrive_expect_tx(&bars.q_full, 2 * Q_BYTES);
         for (int a = 0; a < 8; ++a)
@@ -589,7 +589,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::thread
         tma_load_3d_pair(sbase + 8 * Q_ATOM, &map_qr, 0, rank * HH, bb, bar);
       }
       __syncwarp();
-      i += tiles_of(bb) - (seg == 0 ? jt0 : 0);
+      use = tiles_of(bb) - (seg == 0 ? jt0 : 0);
+      i += use;
     }
   } else if (warp == R::s) {
     // ---------------- score products ----------------

@@ -17,6 +17,11 @@ static_assert(MLA_NOPE == 128 && MLA_VDIM == 128, "key and value widths");
 // nearest, to a copy in the workspace, and begins anew.
 constexpr int kRun = 1024;
 
+// Limit of a wait for the place of the next queries, which are in use for `tiles`
+// key tiles: up to 131,072 of them, of 5.1 us at most (16-bit pages of one row,
+// measured), so 0.67 s on a GPU that does nothing else.
+DEV uint64_t queries_limit_ns(int tiles) { return kWaitLimitNs + (uint64_t)tiles * 50000u; }
+
 template <typename T>
 DEV T* align1024(T* p) {
   return reinterpret_cast<T*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));

@@ -147,7 +147,8 @@ DEV void mbar_arrive_expect_tx_relaxed(uint64_t* bar, uint32_t bytes) {
 // false (after flagging ``*abort`` and the status word) when the limit
 // expires or when another thread of the CTA has already aborted.
 template <bool kCluster = false>
-DEV bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
+DEV bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status,
+                   uint64_t limit_ns = kWaitLimitNs) {
   const uint32_t a = smem_u32(bar);
 #pragma unroll 1
   for (int i = 0; i < 64; ++i)
@@ -158,7 +159,7 @@ DEV bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t*
     for (int i = 0; i < 32; ++i)
       if (kCluster ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity)) return true;
     if (abort && *abort) return false;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+    if (globaltimer_ns() - t0 > limit_ns) {
       if (abort) *abort = 1;
       report_timeout(status);
       return false;
@@ -169,8 +170,9 @@ DEV bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t*
 // The same wait, with a warp-uniform result (the caller then runs
 // .sync.aligned tcgen05 instructions on the outcome).
 template <bool kCluster = false>
-DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
-  const bool ok = mbar_wait<kCluster>(bar, parity, abort, status);
+DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status,
+                   uint64_t limit_ns = kWaitLimitNs) {
+  const bool ok = mbar_wait<kCluster>(bar, parity, abort, status, limit_ns);
   return __all_sync(0xffffffffu, ok);
 }
 

@@ -663,14 +663,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
     // ---------------- queries and keys: each CTA its own, counted by the first ----------------
     const uint32_t q_full0 = mapa_shared(smem_u32(&bars.q_full[0]), 0);
     const uint32_t k_full0 = mapa_shared(smem_u32(&bars.k_full[0]), 0);
-    int u = 0, qn[2] = {0, 0};
+    int u = 0, qn[2] = {0, 0}, use = 0;  // use: key tiles of the item before
     bool ok = true;
     while (ok && range.next(ly, per, &w)) {
       const Block& b = w.b;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (w.count(t) == 0) continue;
-        ok = ok && warp_wait(&bars.q_free[t], (qn[t] & 1) ^ 1, abort, status);
+        ok = ok && warp_wait(&bars.q_free[t], (qn[t] & 1) ^ 1, abort, status,
+                             paged::queries_limit_ns(use));
         if (!ok) break;
         if (lane == 0) {
           if (rank == 0) mbar_arrive_expect_tx(&bars.q_full[t], 2 * Q_BYTES);
@@ -683,6 +684,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::THREADS, 1)
         }
         ++qn[t];
       }
+      use = w.j1 - w.j0;
       const int two = b.two_heads();
       for (int j = w.j0; j < w.j1 && ok; ++j)
         for (int t = two ? 0 : 1; t < 2; ++t) {

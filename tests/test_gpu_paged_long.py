@@ -21,7 +21,7 @@ def shla():
     return m
 
 
-def call(shla, form, bits, q_lens, kv_lens, seed):
+def call(shla, form, bits, q_lens, kv_lens, seed, page=PAGE):
     g = torch.Generator(device="cuda").manual_seed(seed)
     rn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
     rows = torch.empty(POOL, 576, dtype=torch.bfloat16, device="cuda")
@@ -31,15 +31,15 @@ def call(shla, form, bits, q_lens, kv_lens, seed):
     c = torch.ldexp((m * 16).round() / 16, e.clamp(min=-3))
     rows[:, :512], rows[:, 512:] = c, rn(POOL, 64)
     if bits == 16:
-        pages = rows.view(-1, PAGE, 576)
+        pages = rows.view(-1, page, 576)
     else:
-        pages = torch.empty(POOL // PAGE, PAGE, 656, dtype=torch.uint8, device="cuda")
+        pages = torch.empty(POOL // page, page, 656, dtype=torch.uint8, device="cuda")
         slots = torch.arange(POOL, dtype=torch.int32, device="cuda")
         shla.mla_page_write(rows, slots, pages)
         assert torch.equal(shla.mla_page_read(pages, slots), rows)
     N, S = sum(q_lens), len(q_lens)
-    wide = -(-max(kv_lens) // PAGE)
-    table = torch.randint(POOL // PAGE, (S, wide), generator=g, device="cuda").int()
+    wide = -(-max(kv_lens) // page)
+    table = torch.randint(POOL // page, (S, wide), generator=g, device="cuda").int()
     w = (rn(128, 256, 512) * 512 ** -0.5).to(torch.bfloat16)
     status = torch.zeros(2, dtype=torch.int32, device="cuda")
     out = shla.mla_attend_paged(
@@ -74,3 +74,9 @@ def test_absorbed(shla, q, kv, bits):
 ])
 def test_expanded(shla, q, kv):
     call(shla, "expanded", 16, q, kv, 2)
+
+
+def test_the_longest_sequence_in_the_smallest_pages(shla):
+    # 2^24 positions under 148 tokens: a pair's second token waits 0.6 s for the first
+    # one's queries to be done with
+    call(shla, "absorbed", 16, [148], [1 << 24], 3, page=1)

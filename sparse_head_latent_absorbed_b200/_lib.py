@@ -371,11 +371,14 @@ def _pool(pages: torch.Tensor):
     if pages.dim() != 3 or pages.shape[2] != width or pages.stride(2) != 1:
         raise MLAError(f"pages must be [P, page_size, {width}] with unit inner stride")
     P, ps, _ = pages.shape
-    row = pages.stride(1)
-    page = pages.stride(0) if P > 1 else ps * row  # (one page: its stride is never used)
+    size = 1 if kind else 2
+    # (the stride of a dimension of one entry says nothing)
+    row = pages.stride(1) if ps > 1 else width
+    page = pages.stride(0) if P > 1 else ps * row
+    if ps == 1 and page * size < 2 ** 31:
+        row = page
     if min(row, page) < 0 or max(row, page) > 2 ** 31 - 1:
         raise MLAError("page strides out of range")
-    size = 1 if kind else 2
     return pages.data_ptr(), kind, P, ps, page * size, row * size
 
 

@@ -398,6 +398,17 @@ def _bf16(t: torch.Tensor, name: str, shape: tuple, device) -> None:
                        f"{t.dtype} {list(t.shape)} on {t.device}")
 
 
+def _size(v, name: str) -> int:
+    """v as a C int (ctypes would cut it to 32 bits, int() to a whole number)."""
+    try:
+        n = int(v)
+    except (TypeError, ValueError, OverflowError):
+        n = None
+    if n is None or n != v or not -2 ** 31 <= n < 2 ** 31:
+        raise MLAError(f"{name} must be a whole number of 32 bits, got {v}")
+    return n
+
+
 def _status(t: Optional[torch.Tensor], device):
     if t is None:
         return None
@@ -463,7 +474,8 @@ def mla_attend_paged_workspace_bytes(N: int, S: int, max_kv: int, bits: int,
     16-bit pages."""
     if form not in FORMS or bits not in (8, 16):
         raise MLAError(f"form must be one of {', '.join(FORMS)}, bits 8 or 16")
-    return int(LIB.mla_attend_paged_workspace_bytes(int(N), int(S), int(max_kv), int(bits == 8),
+    return int(LIB.mla_attend_paged_workspace_bytes(_size(N, "N"), _size(S, "S"),
+                                                    _size(max_kv, "max_kv"), int(bits == 8),
                                                     FORMS[form]))
 
 
@@ -494,6 +506,7 @@ def mla_attend_paged(q_nope: torch.Tensor, q_pe: torch.Tensor, wkv_b: torch.Tens
         out = torch.empty_like(q_nope)
     else:
         _bf16(out, "out", (N, 128, 128), dev)
+    max_kv = _size(max_kv, "max_kv")
     if N == 0 or S == 0:
         return out
     if ws is not None and (ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != dev):
@@ -509,7 +522,7 @@ def mla_attend_paged(q_nope: torch.Tensor, q_pe: torch.Tensor, wkv_b: torch.Tens
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
     _on_device(dev, "mla_attend_paged", LIB.mla_attend_paged, q_nope.data_ptr(), q_pe.data_ptr(),
                wkv_b.data_ptr(), pool, kind, P, ps, page, row, page_table.data_ptr(),
-               page_table.shape[1], cu_q.data_ptr(), kv_len.data_ptr(), S, N, int(max_kv),
+               page_table.shape[1], cu_q.data_ptr(), kv_len.data_ptr(), S, N, max_kv,
                float(scale), FORMS[form], out.data_ptr(), ws.data_ptr(), ws.numel(),
                _status(status, dev))
     return out

@@ -382,8 +382,10 @@ int mla_query_proj(const mla_bf16_t* x, const mla_bf16_t* wq_a, const mla_bf16_t
  *                   mantissa bits), 4 fp32 scales, 64 bf16 rotary values.  Scale g
  *                   belongs to latent values 128g .. 128g+127; a value is
  *                   code * scale.
- * The pages described on the method's pages are contiguous bf16 only; paging
- * and the 8-bit kind are this library's own.
+ * The pages described on the method's pages are contiguous bf16 only.  The 656
+ * bytes are laid out as in the 8-bit rows that public serving code for latent
+ * attention stores; its scales are commonly max / 448, this library's powers of
+ * two.
  *   pool         16-byte aligned; page p, row o at pool + p*page_stride + o*row_stride
  *   page_stride, row_stride   bytes, multiples of 16; row_stride >= 1152 / 656;
  *                page_stride a multiple of row_stride holding page_size rows;
@@ -404,12 +406,13 @@ int mla_query_proj(const mla_bf16_t* x, const mla_bf16_t* wq_a, const mla_bf16_t
  * max |x| <= 448 * 2^n over the group; a code is x / scale (exact) rounded to
  * nearest even, saturated at 448.  A group with an infinity or NaN gets the
  * scale NaN and codes 0: all its values read as NaN.  A power of two makes code
- * * scale exact in bf16, so the rounding to a code is the only one.  (Rows
- * written by other means keep to this: scales 2^n in that range or NaN, no NaN
- * codes 0x7f, 0xff.)  N >= 0.
+ * * scale exact in bf16, so the rounding to a code is the only one.  N >= 0.
+ * Rows written by other means may hold any fp32 scale: wherever rows are read, a
+ * value is then code * scale in fp32, rounded once more, to bf16.  They hold no
+ * NaN codes (0x7f, 0xff): under a power-of-two scale these read as numbers.
  *
- * mla_page_read returns the rows of slots as bf16 [N] rows (exactly code *
- * scale); slot -1, and any other slot outside the pool (counted in
+ * mla_page_read returns the rows of slots as bf16 [N] rows (code * scale, exactly
+ * for rows of mla_page_write); slot -1, and any other slot outside the pool (counted in
  * status[1]), gives a row of zeros.  The rows written
  * share no memory with the slots read.
  *

@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(256) gather_kernel(const Pool pool, const Layo
           const float sc = __int_as_float(ld_global_nc_s32_early(
               reinterpret_cast<const int32_t*>(src + pages::kScaleOff + (lane >> 3) * 4)));
           if (lane < 8) pe = ld_global_nc_v4(src + pages::kRopeOff + lane * 16);
-          pages::dequant16(c, pages::Factor(sc), x, y);
+          pages::dequant16(c, pages::Factor(sc), pages::needs_fp32(sc), x, y);
         } else {
           x = ld_global_nc_v4(src + lane * 32);
           y = ld_global_nc_v4(src + lane * 32 + 16);

@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(256) page_read_kernel(
           __int_as_float(ld_global_nc_s32_early(reinterpret_cast<const int32_t*>(
               src + kScaleOff + (lane >> 3) * 4)));
       if (lane < 8) pe = ld_global_nc_v4(src + kRopeOff + lane * 16);
-      dequant16(c, Factor(s), a, b);
+      dequant16(c, Factor(s), needs_fp32(s), a, b);
     } else {
       a = ld_global_nc_v4(src + lane * 32);
       b = ld_global_nc_v4(src + lane * 32 + 16);

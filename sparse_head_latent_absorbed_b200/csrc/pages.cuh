@@ -30,7 +30,7 @@ inline int check_pool(const void* pool, int kind, int num_pages, int page_size,
     return MLA_ERR_SHAPE;
   if (!aligned16(pool) || row_stride % 16 || page_stride % 16) return MLA_ERR_ALIGN;
   if (page_stride % row_stride || page_stride / row_stride < page_size) return MLA_ERR_SHAPE;
-  // (bounds the product below: 2^31 pages of at most 2^32 rows each)
+  // (bounds the product below: 2^31 pages of less than 2^31 rows each)
   if (page_stride / row_stride > 0x7fffff00LL) return MLA_ERR_SHAPE;
   if ((int64_t)(num_pages - 1) * (page_stride / row_stride) + page_size > 0x7fffff00LL)
     return MLA_ERR_SHAPE;
@@ -67,7 +67,8 @@ DEV float2 from_e4m3x2(uint32_t codes) {
 // Four codes times a power of two 2^n, n <= 7, as four bf16 values, exactly: a
 // code's sign, exponent and mantissa bits moved into bf16's places read as
 // value * 2^-120 (bf16 subnormals for e4m3 subnormals), so one exact product
-// by f = 2^(120 + n) restores it.  (NaN is in the scale, never in a code.)
+// by f = 2^(120 + n) restores it.  (NaN is in the scale, never in a code: one would
+// read as 480 * 2^n.)
 DEV uint2 dequant4(uint32_t w, __nv_bfloat162 f) {
   const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
   uint32_t lo = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u);
@@ -77,12 +78,21 @@ DEV uint2 dequant4(uint32_t w, __nv_bfloat162 f) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
-// The same for any scale: through fp32.  Out of line, for scales above 2^7.
+// The same for any scale: through fp32, the product rounded to bf16.  Out of
+// line, for scales above 2^7 and for those of rows from elsewhere that are no
+// power of two (where the exact product above would round the scale too).
 static __device__ __noinline__ uint4 dequant8_any(uint2 c, float scale) {
   const float2 a = from_e4m3x2(c.x), b = from_e4m3x2(c.x >> 16);
   const float2 d = from_e4m3x2(c.y), e = from_e4m3x2(c.y >> 16);
   return make_uint4(pack_bf16x2(a.x * scale, a.y * scale), pack_bf16x2(b.x * scale, b.y * scale),
                     pack_bf16x2(d.x * scale, d.y * scale), pack_bf16x2(e.x * scale, e.y * scale));
+}
+
+// whether dequant4 cannot take the scale: anything but 0 and the powers of two from
+// 2^-126 to 2^7
+DEV bool needs_fp32(float scale) {
+  const uint32_t u = __float_as_uint(scale);
+  return u > 0x43000000u || (u & 0x7fffffu) != 0;
 }
 
 // a scale and what dequant4 multiplies by
@@ -93,9 +103,10 @@ struct Factor {
       : scale(s), f(__float2bfloat162_rn(s * 1.329227995784916e36f)) {}  // 2^120
 };
 
-// sixteen codes times a scale as sixteen bf16 values
-DEV void dequant16(const uint4& c, const Factor& f, uint4& o0, uint4& o1) {
-  if (f.scale > 128.f) {
+// sixteen codes times a scale as sixteen bf16 values; fp32: needs_fp32 of the scale
+// (any scale may take that way)
+DEV void dequant16(const uint4& c, const Factor& f, bool fp32, uint4& o0, uint4& o1) {
+  if (fp32) {
     o0 = dequant8_any(make_uint2(c.x, c.y), f.scale);
     o1 = dequant8_any(make_uint2(c.z, c.w), f.scale);
     return;

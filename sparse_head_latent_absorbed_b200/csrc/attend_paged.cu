@@ -514,7 +514,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kE4M3>::thread
           const uint32_t off = j * 256 + (val ? (it >> 2) * 1024 : (it & 1) * 4 * K_ATOM);
           const float f = __shfl_sync(0xffffffffu, sc, s0 + (val ? it * 4 : j * 8 + (it & 1) * 2));
           uint4 o0, o1;
-          pages::dequant16(code[it], pages::Factor(f), fp32, o0, o1);
+          // (an absent row: whatever its codes are, under the factor 0 the exact product is 0)
+          pages::dequant16(code[it], pages::Factor(f), fp32 && f != 0.f, o0, o1);
           st_shared_v4((d0 ^ (j << 5)) + off, o0.x, o0.y, o0.z, o0.w);
           st_shared_v4((d0 ^ (j << 5) ^ 16u) + off, o1.x, o1.y, o1.z, o1.w);
         }

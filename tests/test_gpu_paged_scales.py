@@ -55,3 +55,30 @@ def test_attention(shla, form, q, kv):
         w16 = {**w, "pages": val.view(shape)}
         assert torch.equal(shla.mla_attend_paged(**w, form=form),
                            shla.mla_attend_paged(**w16, form=form))
+
+
+@pytest.mark.parametrize("foreign", [False, True])
+@pytest.mark.parametrize("form", ["absorbed", "expanded"])
+@pytest.mark.parametrize("q,kv,page", [([1, 2, 1], [70, 129, 1], 16), ([1, 1], [200, 65], 7),
+                                       ([130], [150], 64)])
+def test_bytes_that_no_row_uses(shla, form, q, kv, page, foreign):
+    # every byte of free rows is 0xff: NaN codes under NaN scales, the pool's first row
+    # among them
+    w = R.make(q, kv, 16, page, 82, poison=False)
+    P = w["pages"].shape[0]
+    rows = w["pages"].view(-1, 576)
+    stored, val = foreign_rows(rows) if foreign else (R.row8(rows), rows)
+    if not foreign:
+        val = R.values(stored).to(torch.bfloat16)
+    used = torch.zeros(P * page, dtype=torch.bool, device="cuda")
+    for s, n in enumerate(kv):
+        j = torch.arange(n, device="cuda")
+        used[w["page_table"][s].long()[j // page] * page + j % page] = True
+    # a page more, at the front
+    stored = torch.where(used[:, None], stored, torch.full_like(stored, 255))
+    w["pages"] = torch.cat([torch.full_like(stored[:page], 255), stored]).view(P + 1, page, 656)
+    w["page_table"] = w["page_table"] + 1
+    ref = torch.cat([torch.zeros_like(val[:page]), torch.where(used[:, None], val, 0.0)])
+    args = ("q_nope", "q_pe", "wkv_b", "pages", "page_table", "cu_q", "kv_len", "scale")
+    want = R.attend(*({**w, "pages": ref.view(P + 1, page, 576)}[k] for k in args))
+    check(shla.mla_attend_paged(**w, form=form), want)

@@ -412,9 +412,9 @@ int mla_query_proj(const mla_bf16_t* x, const mla_bf16_t* wq_a, const mla_bf16_t
  * NaN codes (0x7f, 0xff): under a power-of-two scale these read as numbers.
  *
  * mla_page_read returns the rows of slots as bf16 [N] rows (code * scale, exactly
- * for rows of mla_page_write); slot -1, and any other slot outside the pool (counted in
- * status[1]), gives a row of zeros.  The rows written
- * share no memory with the slots read.
+ * for rows of mla_page_write); slot -1, and any other slot outside the pool
+ * (counted in status[1]), gives a row of zeros.  The rows written share no memory
+ * with the slots read.
  *
  * Both enqueue one kernel and use no workspace.
  */
@@ -447,7 +447,10 @@ int mla_page_read(const void* pool, int kind, int num_pages, int page_size, int6
  *              from cu_q[S] on (the padding of a captured call) are left as they are
  *   kv_len     int32 [S]; a length above max_kv or the table's reach is cut to it
  *   scale      softmax scale, > 0 (else MLA_ERR_SHAPE)
- *   max_kv     the host's bound on the lengths; sets the workspace's size
+ *   max_kv     the host's bound on the lengths; sets the workspace's size and, in
+ *              the expanded form, how many heads are worked on at a time: close
+ *              to the lengths is faster (256 tokens over 1500 positions: 110 us
+ *              with a bound of 1500 to 65,536, 596 us from 524,289 on)
  *   form       MLA_FORM_ABSORBED folds W_UK into the queries and applies W_UV
  *              after the mix (278,528 flop per token and position).
  *              MLA_FORM_EXPANDED computes every position's keys and values of
@@ -457,19 +460,22 @@ int mla_page_read(const void* pool, int kind, int num_pages, int page_size, int6
  *              (<= 4096) or 208 new tokens a sequence on, where S * max_kv, each
  *              length rounded up to 128, is at most 2^21 (its workspace then
  *              takes up to 11 GB) or the absorbed form is refused.  The forms
- *              agree within rounding.
+ *              agree within rounding.  One form serves the whole call: decode
+ *              tokens and a prompt chunk are faster in a call each (63 tokens
+ *              over 1000 to 7820 positions with a chunk of 512 over 6000: 743
+ *              us in one, 592 in two).
  *   ws         at least mla_attend_paged_workspace_bytes(N, S, max_kv, kind,
  *              form) bytes, 256-byte aligned; contents need not be initialised
  *   O and ws   share no memory with each other and with the arguments that are
  *              read (else MLA_ERR_OVERLAP; the pool's rows, which may lie among
  *              other memory, are not looked at)
  *   status     optional int32[2].  An entry of page_table outside [0, num_pages)
- *              for a page below a sequence's length reads as a page of zeros
- *              and is counted once in status[1].
+ *              for a page below the length of a sequence with new tokens reads
+ *              as a page of zeros and is counted once in status[1].
  * Cached values at positions below kv_len[s] are taken to be finite: a NaN
  * there makes the tokens that see it NaN, an infinity may, and both may do so to
- * earlier tokens of the same sequence in the call.  What the pages hold from kv_len[s] on does not
- * matter.
+ * earlier tokens of the same sequence in the call.  What the pages hold from
+ * kv_len[s] on does not matter.
  * 1 <= N <= 65535, 1 <= S <= 65535, 1 <= max_kv <= 2^24; absorbed: N *
  * ceil(max_kv / 128) < 2^30; expanded: S * max_kv, each length rounded up to
  * 128, at most 2^26 (else MLA_ERR_SHAPE).  The expanded form's workspace holds
@@ -485,7 +491,8 @@ int mla_page_read(const void* pool, int kind, int num_pages, int page_size, int6
  * added to nearest, every 2^17 positions.
  * Rounded to bf16, as tensor-core operands: softmax weights; absorbed: q~, the
  * mixed latent and a split token's partial mixed latents; expanded: keys,
- * values and the partial outputs of work that is split between SMs.  On one device a call gives the same bits every time.
+ * values and the partial outputs of work that is split between SMs.  On one
+ * device a call gives the same bits every time.
  *
  * The kernels of a call are enqueued on `stream`, some under programmatic
  * dependent launch (as described for mla_decode, with the same stream

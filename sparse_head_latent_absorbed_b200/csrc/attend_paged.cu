@@ -152,16 +152,20 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Seqs q, const Pool poo
 // to bf16 as a tensor-core operand (its row sum is of the fp32 P).
 //
 // Bounds, per tile and pair: 147 KB of cache (1.67 us at the measured copy rate
-// for 16-bit pages), 2196 cycles of products (measured alone, and not slower
-// with the loads running: 36 x 33 + 16 x 65; 1.14 us at 1.92 GHz).  Shared
+// for 16-bit pages), 2228 cycles of products (measured alone, and not slower
+// with the loads running: 36 x 33 + 16 x 65; 1.16 us at 1.92 GHz).  Shared
 // memory holds one tile of keys and one of values, in three chunks of 192
 // columns and two of 64 keys, each reloaded as soon as its products are done:
 // the next tile's first chunk lands while this tile's last is in use, so the
 // reload waits neither for the softmax nor for the rest of the tile.
-// Measured: 64 sequences of 1000 to 8000 positions, 16-bit pages, one token each:
-// 83 us for 348 MB (4.2 TB/s; half of the tensor pipe's cycles), about 2800 cycles
-// a tile; the rest is what a tile's chain from scores to weights to values, and the
-// reload of its keys, leave idle.  8-bit pages, 128 sequences up to 16000: 441 us.
+// Measured (clock stamps of every pair): 64 sequences of 1000 to 8000 positions,
+// 16-bit pages, one token each: 82 us for 348 MB (4.2 TB/s; 55% of the tensor pipe's
+// cycles), 28 to 33 tiles a pair in 132,000 cycles at 1.68 GHz: 15,000 until the first
+// tile's values are multiplied, 3200 a tile after another of the same token (3600
+// with the slow ones), 9300 where the token changes, 6400 from the last tile to the
+// end.  What a tile takes beyond its products is its chain from scores to weights to
+// values and the reload of its keys.  8-bit pages, 128 sequences up to 16000: 444 us,
+// 114 to 120 tiles a pair in 803,000 cycles, 6700 a tile, 14,500 at a change.
 // There a tile's place in shared memory is filled by the converting warps, and
 // waiting for the place, loading, converting (50 of 280 us, with four tokens each),
 // storing (40) and the softmax add up; tiles of 64 keys with two places took longer.

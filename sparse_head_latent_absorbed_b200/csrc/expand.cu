@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(1024) layout_kernel(const Seqs q, const Pool p
 // gather: row ly.row[s] + t = position t of sequence s as bf16, zeros from
 // kv[s] to the next multiple of 128 and for entries outside the pool (counted
 // once a page).  One warp per row; bound by memory (128000 8-bit rows, 231 MB, in
-// 41 us; four rows a warp took the same).  `table`, if there is one:
+// 41 to 47 us; four rows a warp took the same).  `table`, if there is one:
 // the rows' table as pages of 64.
 // ===========================================================================
 constexpr int kStagedPage = 64;
@@ -482,12 +482,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm::THREADS, 1)
 // The list of items (a block and a head or two) is cut into one range of equal
 // cost for each pair; what a cut leaves is joined by the next kernel.  (Whole items
 // dealt out in turn: 128 for 74 pairs take two turns, 14% of the time idle.)
-// Measured: 512 tokens over 6000 positions, 128 heads, 195 us (1.24 PFLOP/s); 1024
-// over 32768, 1980 us at 1.55 to 1.6 GHz, where the power limit holds the clock.  What
-// bounds the cycles is a tile's chain: 1480 of softmax (1024 of them its 128
-// exponentials a thread), about 400 until both CTAs' weights are known to the
-// issuer, then its own products while the other tile's wait; two tiles take 3350
-// cycles, their products 2580.  TMEM has no room for a third.
+// Measured (clock stamps of every pair): 512 tokens over 6000 positions, 128 heads,
+// 78 to 85 steps of two tiles a pair in 316,000 cycles: 195 us at 1.62 GHz (1.24
+// PFLOP/s), 222 at 1.42; 1024 over 32768, 879 steps in 3.1 million cycles, 2000 us at
+// 1.56 GHz, 2250 at 1.38: the power limit holds the clock.  What bounds the cycles is a
+// tile's chain: 1480 of softmax (1024 of them its 128 exponentials a thread), about
+// 400 until both CTAs' weights are known to the issuer, then its own products while
+// the other tile's wait; two tiles take 3480 cycles, their products 2580, and the
+// first two of an item 6900.  TMEM has no room for a third tile.
 // Warps 0-3 and 4-7: softmax and output of tile 0 and 1; warp 8: queries and
 // keys by TMA; warp 9: MMA (of the pair's first CTA); warp 10: values by TMA.
 // TMEM: scores [0,128) [128,256), outputs [256,384) [384,512).
@@ -1140,6 +1142,10 @@ struct Ws {
   int heads;  // of a group
 };
 
+// (By the bound, which is all the host knows: under one far above the lengths the
+// groups are small and what a group costs at least shows.  256 tokens over 1500
+// positions: 110 us under a bound of 65,536 positions, 150 under 131,072, 193 under
+// 262,144, 596 from 524,289 on, where sixteen groups of eight heads follow each other.)
 static Ws layout(int N, int S, int max_kv) {
   Ws w;
   w.r = rows_ws(N, S, max_kv);

@@ -1,8 +1,10 @@
 // Writing rows into a paged latent cache and reading them back, in 8 or 16
 // bits.  Both are bound by memory: a row is read once and written once
 // (1152 B on the bf16 side, 656 or 1152 B on the page side).  Measured from a cold
-// L2, 8-bit pages: 16384 rows written in 10 us (4.5 at the copy rate), 32768 read
-// in 14 us (9.1); a few rows in 6, which is a launch.
+// L2: 16384 rows written in 10 us (8 bits; 4.5 at the copy rate) and 10 to 12 (16
+// bits; 5.8), 32768 read in 16 us (9.1) and 18 (11.5); a few rows in 6, which is a
+// launch.  A warp's one row (its slot, then its address, then its store) has
+// nothing in flight behind it.
 #include "pages.cuh"
 
 namespace shla {
